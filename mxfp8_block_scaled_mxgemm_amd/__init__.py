@@ -11,3 +11,8 @@ from ._lib import (  # noqa: F401
     MxgemmError, Options, Plan, SegGemm, decode,
     last_error, load, options, plan, quantize_mxfp8, quantize_segments, run_static,
 )
+from ._moe import (  # noqa: F401
+    EXPORTED_MOE, LinearGrads, TokenSort, combine_tokens, combine_tokens_backward, dispatch_tokens,
+    dispatch_tokens_backward, dispatch_tokens_mx, epilogue_backward, linear, linear_backward, linear_by_inner,
+    quantize_transposed, sort_tokens,
+)

@@ -15,9 +15,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxgemm_seg.so")
 
-# One GEMM translation unit per (A, B) FP8 format pair, compiled in parallel.
+# One GEMM (and one fused-product) translation unit per pair of FP8 formats,
+# compiled in parallel.
 SOURCES = ["kernels.hip", "gemm_e4m3_e4m3.hip", "gemm_e5m2_e5m2.hip", "gemm_e4m3_e5m2.hip",
-           "gemm_e5m2_e4m3.hip", "ring.hip", "mxgemm_seg.cpp"]
+           "gemm_e5m2_e4m3.hip", "ring.hip", "mxgemm_seg.cpp", "tokens.hip", "grad.hip",
+           "linear_e4m3_e4m3.hip", "linear_e5m2_e5m2.hip", "linear_e4m3_e5m2.hip",
+           "linear_e5m2_e4m3.hip", "moe.cpp"]
 ARCH = "gfx950"
 
 # Packed-FP32 ALU forms are switched off for every kernel (the compiler would

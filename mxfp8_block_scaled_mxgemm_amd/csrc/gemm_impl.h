@@ -770,13 +770,18 @@ __host__ __device__ constexpr int copies_in_part(int part, int nparts)
 // (pairs of them summed fresh).  At the end groups 1 .. WGK - 1 pass their
 // totals through LDS and group 0 adds them in group order and stores the
 // tile.  The work item's K-steps must be a multiple of WGK.
-template <int BM, int BN, int WGM, int WGN, int WGK, int OCC, int FA, int FB>
-__global__ void __launch_bounds__(WGM * WGN * WGK * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
-mxgemm_exact_kernel(GemmArgs p)
+// Its K loop: sums the K-steps of one K group into `tot`.  src_of(s): the
+// sources of the group's K-step s.  With RAGGED only the first `valid` of the
+// nsteps steps (at least nsteps - 1 of them) are the group's own, and src_of
+// stays in range for the others.  On return this wave's copies have landed.
+template <int BM, int BN, int WGM, int WGN, int WGK, int FA, int FB, bool RAGGED, class Src>
+__device__ __forceinline__ void exact_mainloop(uint8_t* stage0, uint8_t* stage1,
+                                               const CopyOffsets<BM, BN, WGM * WGN, 32>& co, const Src& src_of,
+                                               int nsteps, int valid, int wk, int wl, int lane,
+                                               v16f (&tot)[BM / WGM / 32][BN / WGN / 32])
 {
     constexpr int MW = 32;
     constexpr int NWG = WGM * WGN;         // waves of one K group
-    constexpr int NW = NWG * WGK;
     constexpr int TM = BM / WGM, TN = BN / WGN;
     constexpr int GA = TM / MW, GB = TN / MW;
     constexpr int NF = GA + GB;            // fragments a wave reads per sub-step
@@ -786,14 +791,6 @@ mxgemm_exact_kernel(GemmArgs p)
     // upper bound of the work slices of one MFMA group (see kstep)
     constexpr int kMaxTasks = 20 + StageGeom<BM, BN, NWG>::JA + StageGeom<BM, BN, NWG>::JB + 4 + 2;
     typedef StageGeom<BM, BN, NWG> G;      // one K-step, copied by one K group
-
-    __shared__ __attribute__((aligned(1024))) uint8_t stage0[WGK * G::STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t stage1[WGK * G::STAGE];
-
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform
-    const int wk = wave / NWG, wl = wave % NWG;                  // K group, wave in the group
     const int wm = wl / WGN, wn = wl % WGN;
     const int lr = lane & 31, lq = lane >> 5;
     const int ksub = wk * G::STAGE;        // the group's K-step within a stage
@@ -809,6 +806,182 @@ mxgemm_exact_kernel(GemmArgs p)
     auto scale_off = [&](int f) { return f < GA ? sa_row + f * MW * 4 : sb_row + (f - GA) * MW * 4; };
     auto chunk_off = [&](int j) { return swz_t<MW>(lr, 2 * j + lq) * 16; };
 
+    v16f acc[GA][GB];          // MFMA accumulators of the current pair of K-steps
+#pragma unroll
+    for (int i = 0; i < GA; ++i)
+#pragma unroll
+        for (int g = 0; g < GB; ++g)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                acc[i][g][v] = 0.f;
+                tot[i][g][v] = 0.f;
+            }
+    auto flush = [&]() {
+#pragma unroll
+        for (int i = 0; i < GA; ++i)
+#pragma unroll
+            for (int g = 0; g < GB; ++g)
+                tot[i][g] += acc[i][g];
+    };
+
+    u32x4 raw[NF];             // codes of the sub-step after the next
+    u32x4 cva[GA][2];          // A operands (bfloat16 pairs) of the current sub-step
+    u32x4 cvb[2][GB][2];       // B operands, by sub-step parity
+    uint32_t sw[NF];           // scale words (4 MX blocks) of a K-step
+
+    copy_issue(co, src_of(0), stage0 + ksub, wl);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (nsteps > 1)
+        copy_issue(co, src_of(1), stage1 + ksub, wl);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        sw[f] = *reinterpret_cast<const uint32_t*>(stage0 + scale_off(f));
+        raw[f] = *reinterpret_cast<const u32x4*>(stage0 + frag_off(f) + chunk_off(0));
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        const float sc = e8m0_to_f32(sw[f]);
+        u32x4(&dst)[2] = f < GA ? cva[f] : cvb[0][f - GA];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            dst[e >> 2][e & 3] = f < GA ? cvt_word<FA>(raw[f], sc, e) : cvt_word<FB>(raw[f], sc, e);
+        raw[f] = *reinterpret_cast<const u32x4*>(stage0 + frag_off(f) + chunk_off(1));
+    }
+
+    // Group i of a sub-step: the 2 GB MFMAs of A fragment i, each
+    // followed by a slice of the group's other work, in this order:
+    //   A fragment i: scale, 8 conversions (next sub-step), LDS read
+    //     (the sub-step after);
+    //   the B fragments assigned to group i: the same;
+    //   at sub-step 2: this group's share of the copies of step s + 2,
+    //     and the scale words of step s + 1 for fragments f = i mod GA.
+    // sched_barrier fences keep that order, so the conversions run in
+    // the MFMAs' shadow.
+    // FRESH: the first K-step of a pair, whose first MFMA per output
+    // block starts from a zero accumulator.
+    auto kstep = [&](auto fresh, int s, const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt) {
+        constexpr bool FRESH = decltype(fresh)::value;
+        // Past the last K-step the copies repeat the last one (into the
+        // stage just released, never read again): no branches here.
+        const StepSrc src2 = src_of(s + 2 < nsteps ? s + 2 : nsteps - 1);
+        uint32_t swn[NF];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = j & 1;
+            if (j == 2) {
+                // every wave has read all of CUR and has its copies of
+                // step s + 1 in NXT
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+            }
+            // Sub-steps j + 1, j + 2 are converted and read even past
+            // the last K-step (then from the idle stage NXT; the values
+            // are never used), which keeps this code branch-free.
+            const uint8_t* src = j < 2 ? cur : nxt;
+            const int coff = chunk_off((j + 2) & 3);
+            const int jn = (j + 1) & 3;
+#pragma unroll
+            for (int i = 0; i < GA; ++i) {
+                constexpr int NU = 2 * GB;                        // MFMAs in the group
+                constexpr int RB = GA / GB;                       // groups per B fragment
+                const int nbf = i % RB == 0 ? 1 : 0;              // B fragment i / RB is the group's
+                const int gb = i / RB;
+                const int ncopy = j == 2 ? copies_in_part<BM, BN, NWG>(i, GA) : 0;
+                const int nsw = j == 2 ? 1 + (i + GA < NF ? 1 : 0) : 0;   // fragments i, i + GA
+                const int ntask = 10 * (1 + nbf) + ncopy + nsw;
+                u32x4 cva_n[2];
+                float sc = 0.f;
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const int m = u / GB, g = u % GB;
+                    acc[i][g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(v8bf, cvb[c][g][m]), __builtin_bit_cast(v8bf, cva[i][m]),
+                        (FRESH && j == 0 && m == 0) ? v16f{} : acc[i][g], 0, 0, 0);
+                    const int t0 = u * ntask / NU, t1 = (u + 1) * ntask / NU;
+#pragma unroll
+                    for (int t = 0; t < kMaxTasks; ++t) {
+                        if (t < t0 || t >= t1)
+                            continue;
+                        if (t < 10) {                              // A fragment i
+                            if (t == 0)
+                                sc = e8m0_to_f32(sw[i] >> (8 * jn));
+                            else if (t < 9)
+                                cva_n[(t - 1) >> 2][(t - 1) & 3] = cvt_word<FA>(raw[i], sc, t - 1);
+                            else
+                                raw[i] = *reinterpret_cast<const u32x4*>(src + frag_off(i) + coff);
+                        } else if (t < 10 * (1 + nbf)) {           // B fragment gb
+                            const int tb = t - 10;
+                            if (tb == 0)
+                                sc = e8m0_to_f32(sw[GA + gb] >> (8 * jn));
+                            else if (tb < 9)
+                                cvb[c ^ 1][gb][(tb - 1) >> 2][(tb - 1) & 3] = cvt_word<FB>(raw[GA + gb], sc, tb - 1);
+                            else
+                                raw[GA + gb] = *reinterpret_cast<const u32x4*>(src + frag_off(GA + gb) + coff);
+                        } else if (t < 10 * (1 + nbf) + ncopy) {   // copies of step s + 2
+                            copy_one(co, src2, const_cast<uint8_t*>(cur) + ksub, wl, i, GA, t - 10 * (1 + nbf));
+                        } else {                                   // scale words of step s + 1
+                            const int f2 = i + GA * (t - 10 * (1 + nbf) - ncopy);
+                            swn[f2] = *reinterpret_cast<const uint32_t*>(nxt + scale_off(f2));
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                cva[i][0] = cva_n[0];
+                cva[i][1] = cva_n[1];
+            }
+            if (j == 2) {
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    sw[f] = swn[f];
+            }
+        }
+    };
+    // A K group with one step less than the others still meets the barrier
+    // of the last one.
+    auto idle = [&]() {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    };
+    int s = 0;
+    for (; s + 1 < nsteps; s += 2) {
+        kstep(std::true_type(), s, stage0, stage1);
+        if (!RAGGED || s + 1 < valid)
+            kstep(std::false_type(), s + 1, stage1, stage0);
+        else
+            idle();
+        flush();
+    }
+    if (s < nsteps) {
+        if (!RAGGED || s < valid) {
+            kstep(std::true_type(), s, stage0, stage1);
+            flush();
+        } else {
+            idle();
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the work-group
+}
+
+template <int BM, int BN, int WGM, int WGN, int WGK, int OCC, int FA, int FB>
+__global__ void __launch_bounds__(WGM * WGN * WGK * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+mxgemm_exact_kernel(GemmArgs p)
+{
+    constexpr int MW = 32;
+    constexpr int NWG = WGM * WGN;         // waves of one K group
+    constexpr int NW = NWG * WGK;
+    constexpr int TM = BM / WGM, TN = BN / WGN;
+    constexpr int GA = TM / MW, GB = TN / MW;
+    typedef StageGeom<BM, BN, NWG> G;      // one K-step, copied by one K group
+
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[WGK * G::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[WGK * G::STAGE];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform
+    const int wk = wave / NWG, wl = wave % NWG;                  // K group, wave in the group
+    const int wm = wl / WGN, wn = wl % WGN;
     // one work item per work-group (the dispatcher does the load balancing;
     // a persistent loop would hold the epilogue's per-lane address terms in
     // registers across the K loop)
@@ -825,149 +998,9 @@ mxgemm_exact_kernel(GemmArgs p)
         const int nsteps = p.segs_per_split * (p.kpr / kBK) / WGK;
         auto src_of = [&](int s) { return step_src(p, seg0, n0, WGK * s + wk); };
 
-        v16f acc[GA][GB];          // MFMA accumulators of the current pair of K-steps
         v16f tot[GA][GB];          // running totals of the finished pairs
-#pragma unroll
-        for (int i = 0; i < GA; ++i)
-#pragma unroll
-            for (int g = 0; g < GB; ++g)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    acc[i][g][v] = 0.f;
-                    tot[i][g][v] = 0.f;
-                }
-        auto flush = [&]() {
-#pragma unroll
-            for (int i = 0; i < GA; ++i)
-#pragma unroll
-                for (int g = 0; g < GB; ++g)
-                    tot[i][g] += acc[i][g];
-        };
-
-        u32x4 raw[NF];             // codes of the sub-step after the next
-        u32x4 cva[GA][2];          // A operands (bfloat16 pairs) of the current sub-step
-        u32x4 cvb[2][GB][2];       // B operands, by sub-step parity
-        uint32_t sw[NF];           // scale words (4 MX blocks) of a K-step
-
-        copy_issue(co, src_of(0), stage0 + ksub, wl);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (nsteps > 1)
-            copy_issue(co, src_of(1), stage1 + ksub, wl);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            sw[f] = *reinterpret_cast<const uint32_t*>(stage0 + scale_off(f));
-            raw[f] = *reinterpret_cast<const u32x4*>(stage0 + frag_off(f) + chunk_off(0));
-        }
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const float sc = e8m0_to_f32(sw[f]);
-            u32x4(&dst)[2] = f < GA ? cva[f] : cvb[0][f - GA];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                dst[e >> 2][e & 3] = f < GA ? cvt_word<FA>(raw[f], sc, e) : cvt_word<FB>(raw[f], sc, e);
-            raw[f] = *reinterpret_cast<const u32x4*>(stage0 + frag_off(f) + chunk_off(1));
-        }
-
-        // Group i of a sub-step: the 2 GB MFMAs of A fragment i, each
-        // followed by a slice of the group's other work, in this order:
-        //   A fragment i: scale, 8 conversions (next sub-step), LDS read
-        //     (the sub-step after);
-        //   the B fragments assigned to group i: the same;
-        //   at sub-step 2: this group's share of the copies of step s + 2,
-        //     and the scale words of step s + 1 for fragments f = i mod GA.
-        // sched_barrier fences keep that order, so the conversions run in
-        // the MFMAs' shadow.
-        // FRESH: the first K-step of a pair, whose first MFMA per output
-        // block starts from a zero accumulator.
-        auto kstep = [&](auto fresh, int s, const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt) {
-            constexpr bool FRESH = decltype(fresh)::value;
-            // Past the last K-step the copies repeat the last one (into the
-            // stage just released, never read again): no branches here.
-            const StepSrc src2 = src_of(s + 2 < nsteps ? s + 2 : nsteps - 1);
-            uint32_t swn[NF];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = j & 1;
-                if (j == 2) {
-                    // every wave has read all of CUR and has its copies of
-                    // step s + 1 in NXT
-                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                    __syncthreads();
-                }
-                // Sub-steps j + 1, j + 2 are converted and read even past
-                // the last K-step (then from the idle stage NXT; the values
-                // are never used), which keeps this code branch-free.
-                const uint8_t* src = j < 2 ? cur : nxt;
-                const int coff = chunk_off((j + 2) & 3);
-                const int jn = (j + 1) & 3;
-#pragma unroll
-                for (int i = 0; i < GA; ++i) {
-                    constexpr int NU = 2 * GB;                        // MFMAs in the group
-                    constexpr int RB = GA / GB;                       // groups per B fragment
-                    const int nbf = i % RB == 0 ? 1 : 0;              // B fragment i / RB is the group's
-                    const int gb = i / RB;
-                    const int ncopy = j == 2 ? copies_in_part<BM, BN, NWG>(i, GA) : 0;
-                    const int nsw = j == 2 ? 1 + (i + GA < NF ? 1 : 0) : 0;   // fragments i, i + GA
-                    const int ntask = 10 * (1 + nbf) + ncopy + nsw;
-                    u32x4 cva_n[2];
-                    float sc = 0.f;
-#pragma unroll
-                    for (int u = 0; u < NU; ++u) {
-                        const int m = u / GB, g = u % GB;
-                        acc[i][g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(v8bf, cvb[c][g][m]), __builtin_bit_cast(v8bf, cva[i][m]),
-                            (FRESH && j == 0 && m == 0) ? v16f{} : acc[i][g], 0, 0, 0);
-                        const int t0 = u * ntask / NU, t1 = (u + 1) * ntask / NU;
-#pragma unroll
-                        for (int t = 0; t < kMaxTasks; ++t) {
-                            if (t < t0 || t >= t1)
-                                continue;
-                            if (t < 10) {                              // A fragment i
-                                if (t == 0)
-                                    sc = e8m0_to_f32(sw[i] >> (8 * jn));
-                                else if (t < 9)
-                                    cva_n[(t - 1) >> 2][(t - 1) & 3] = cvt_word<FA>(raw[i], sc, t - 1);
-                                else
-                                    raw[i] = *reinterpret_cast<const u32x4*>(src + frag_off(i) + coff);
-                            } else if (t < 10 * (1 + nbf)) {           // B fragment gb
-                                const int tb = t - 10;
-                                if (tb == 0)
-                                    sc = e8m0_to_f32(sw[GA + gb] >> (8 * jn));
-                                else if (tb < 9)
-                                    cvb[c ^ 1][gb][(tb - 1) >> 2][(tb - 1) & 3] = cvt_word<FB>(raw[GA + gb], sc, tb - 1);
-                                else
-                                    raw[GA + gb] = *reinterpret_cast<const u32x4*>(src + frag_off(GA + gb) + coff);
-                            } else if (t < 10 * (1 + nbf) + ncopy) {   // copies of step s + 2
-                                copy_one(co, src2, const_cast<uint8_t*>(cur) + ksub, wl, i, GA, t - 10 * (1 + nbf));
-                            } else {                                   // scale words of step s + 1
-                                const int f2 = i + GA * (t - 10 * (1 + nbf) - ncopy);
-                                swn[f2] = *reinterpret_cast<const uint32_t*>(nxt + scale_off(f2));
-                            }
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                    cva[i][0] = cva_n[0];
-                    cva[i][1] = cva_n[1];
-                }
-                if (j == 2) {
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-                        sw[f] = swn[f];
-                }
-            }
-        };
-        int s = 0;
-        for (; s + 1 < nsteps; s += 2) {
-            kstep(std::true_type(), s, stage0, stage1);
-            kstep(std::false_type(), s + 1, stage1, stage0);
-            flush();
-        }
-        if (s < nsteps) {
-            kstep(std::true_type(), s, stage0, stage1);
-            flush();
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the work-group
+        exact_mainloop<BM, BN, WGM, WGN, WGK, FA, FB, false>(stage0, stage1, co, src_of, nsteps, nsteps, wk, wl,
+                                                             lane, tot);
 
         if constexpr (WGK > 1) {
             // groups 1 .. WGK - 1 pass their totals through stage 0

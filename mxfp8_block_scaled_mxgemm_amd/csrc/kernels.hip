@@ -2,6 +2,7 @@
 // reduction, the MXFP8 quantiser, the tile table, and the dispatch to the
 // GEMM kernels (gemm_impl.h, one translation unit per FP8 format pair).
 #include "device_util.h"
+#include "quant.h"
 #include "schedule.h"
 
 namespace mxg {
@@ -181,83 +182,6 @@ hipError_t launch_gemm(int cfg, bool exact, int fa, int fb, const GemmArgs& a, h
 }
 
 // ------------------------------------------------------------- quantiser --
-
-// E4M3 (OCP "FN") code of a non-NaN float, round-to-nearest-even, sign of
-// zero kept; magnitudes above 448 after rounding (infinities included)
-// saturate to 448 (code 0x7E).  Normal range: keep 3 mantissa bits and
-// round on the 20 dropped bits; below 2^-6 the grid step is 2^-9, so
-// y * 512 rounded to an integer is the code (8 is the smallest normal,
-// code 0x08).
-__device__ __forceinline__ uint32_t e4m3_rne(float y)
-{
-    const uint32_t u = __float_as_uint(y);
-    const uint32_t sign = (u >> 24) & 0x80u;
-    const uint32_t a = u & 0x7FFFFFFFu;
-    uint32_t code;
-    if (a < 0x3C800000u) {                       // |y| < 2^-6
-        code = (uint32_t)rintf(__uint_as_float(a) * 512.0f);
-    } else {
-        const uint32_t keep = (a >> 20) & 7u;
-        const uint32_t rest = a & 0xFFFFFu;
-        code = (((a >> 23) - 120u) << 3) | keep;  // biased exponent 127 -> 7
-        if (rest > 0x80000u || (rest == 0x80000u && (keep & 1u)))
-            code += 1u;
-        if (code > 0x7Eu)
-            code = 0x7Eu;
-    }
-    return code | sign;
-}
-
-// E5M2 (OCP, bias 15) code of a float, round-to-nearest-even, saturating at
-// the largest finite value 57344 (code 0x7B) instead of producing infinity.
-// Normal range: keep 2 mantissa bits and round on the 21 dropped bits;
-// below 2^-14 the grid step is 2^-16, so y * 65536 rounded to an integer is
-// the code (4 is the smallest normal, code 0x04).
-__device__ __forceinline__ uint32_t e5m2_rne(float y)
-{
-    const uint32_t u = __float_as_uint(y);
-    const uint32_t sign = (u >> 24) & 0x80u;
-    const uint32_t a = u & 0x7FFFFFFFu;
-    uint32_t code;
-    if (a < 0x38800000u) {                       // |y| < 2^-14
-        code = (uint32_t)rintf(__uint_as_float(a) * 65536.0f);
-    } else {
-        const uint32_t keep = (a >> 21) & 3u;
-        const uint32_t rest = a & 0x1FFFFFu;
-        code = (((a >> 23) - 112u) << 2) | keep;  // biased exponent 127 -> 15
-        if (rest > 0x100000u || (rest == 0x100000u && (keep & 1u)))
-            code += 1u;
-        if (code > 0x7Bu)
-            code = 0x7Bu;
-    }
-    return code | sign;
-}
-
-// Smallest e with fmax * 2^e >= amax, clamped to [-127, 127], for the
-// format's largest finite value fmax = 1.75 * 2^EMAX (448: EMAX = 8 for
-// E4M3; 57344: EMAX = 15 for E5M2).  With amax = 1.m * 2^x, e = x - EMAX
-// when 1.m <= 1.75, else x - EMAX + 1.  Zero and float32 subnormals give
-// -127 (the clamp), +inf gives 127 (the clamp of an unbounded e); amax is
-// never NaN here (NaN blocks are handled by the caller).
-template <int EMAX>
-__device__ __forceinline__ int e8m0_exponent(float amax)
-{
-    const uint32_t u = __float_as_uint(amax);
-    const int ex = (int)(u >> 23);
-    if (ex == 0)
-        return -127;
-    if (ex == 255)
-        return 127;
-    int e = ex - 127 - EMAX + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    e = e < -127 ? -127 : e;
-    return e > 127 ? 127 : e;
-}
-
-template <int F>
-__device__ __forceinline__ uint32_t fp8_rne(float y)
-{
-    return F == kE5M2 ? e5m2_rne(y) : e4m3_rne(y);
-}
 
 // Eight threads per 32-element block, four elements each.  The block's
 // amax is the largest |x| bit pattern: for non-negative floats the integer

@@ -1,0 +1,6 @@
+// The product's kernels for A E4M3, W E4M3.
+#include "linear_impl.h"
+
+namespace mxg {
+template hipError_t launch_linear_fmt<kE4M3, kE4M3>(int, bool, const LinArgs&, hipStream_t);
+}

@@ -1,0 +1,6 @@
+// The product's kernels for A E5M2, W E5M2.
+#include "linear_impl.h"
+
+namespace mxg {
+template hipError_t launch_linear_fmt<kE5M2, kE5M2>(int, bool, const LinArgs&, hipStream_t);
+}

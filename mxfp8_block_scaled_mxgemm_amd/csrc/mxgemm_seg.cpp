@@ -13,12 +13,13 @@
 #include <string>
 #include <vector>
 
+#include "host_util.h"
 #include "kernels.h"
 #include "schedule.h"
 
-namespace {
+namespace mxg {
 
-thread_local std::string g_err;
+static thread_local std::string g_err;
 
 int fail(int code, const char* fmt, ...)
 {
@@ -27,21 +28,42 @@ int fail(int code, const char* fmt, ...)
     va_start(ap, fmt);
     vsnprintf(buf, sizeof(buf), fmt, ap);
     va_end(ap);
-    g_err = buf;
+    try {
+        g_err = buf;
+    } catch (...) {
+        g_err.clear();   // no memory for the message: the code still says it
+    }
     return code;
 }
 
-// A failing HIP call is reported through the return code and the message;
-// the thread's last HIP error is cleared so that a later, unrelated launch
-// check does not report it again.
-#define HIP_TRY(expr)                                                                   \
-    do {                                                                                \
-        hipError_t e_ = (expr);                                                         \
-        if (e_ != hipSuccess) {                                                         \
-            (void)hipGetLastError();                                                    \
-            return fail(MXGEMM_EHIP, "%s failed: %s", #expr, hipGetErrorString(e_));    \
-        }                                                                               \
-    } while (0)
+// Pageable host memory would fault the kernels, so it is refused before
+// anything is enqueued.
+int gpu_accessible(const void* p, const char* name, int device)
+{
+    hipPointerAttribute_t at;
+    hipError_t e = hipPointerGetAttributes(&at, p);
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(MXGEMM_EINVAL, "%s: no pointer attributes (%s)", name, hipGetErrorString(e));
+    }
+    if (at.type == hipMemoryTypeDevice) {
+        if (at.device != device)
+            return fail(MXGEMM_EINVAL, "%s is memory of device %d, not of device %d", name, at.device,
+                        device);
+        return MXGEMM_OK;
+    }
+    if (at.type == hipMemoryTypeManaged || at.type == hipMemoryTypeHost)
+        return MXGEMM_OK;
+    return fail(MXGEMM_EINVAL, "%s is not memory the GPU can access (host memory that is not "
+                "pinned?)", name);
+}
+
+}  // namespace mxg
+
+using mxg::fail;
+using mxg::gpu_accessible;
+
+namespace {
 
 bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -417,33 +439,11 @@ void release(mxgemm_seg* h)
 }
 
 // The run() buffers must be memory the GPU can read: device memory of the
-// handle's device, managed memory or pinned host memory.  Pageable host
-// memory would fault the kernels, so it is refused before anything is
-// enqueued.  Checked whenever the pointers differ from the last ones that
-// passed (so a steady loop, and graph capture after an eager run, make no
-// extra calls).  Buffer sizes are the caller's contract and are not
-// checked: an allocation's range as the runtime reports it need not be all
-// of the memory mapped behind a pointer.
-int gpu_accessible(const void* p, const char* name, int device)
-{
-    hipPointerAttribute_t at;
-    hipError_t e = hipPointerGetAttributes(&at, p);
-    if (e != hipSuccess) {
-        (void)hipGetLastError();
-        return fail(MXGEMM_EINVAL, "%s: no pointer attributes (%s)", name, hipGetErrorString(e));
-    }
-    if (at.type == hipMemoryTypeDevice) {
-        if (at.device != device)
-            return fail(MXGEMM_EINVAL, "%s is memory of device %d, not of device %d", name, at.device,
-                        device);
-        return MXGEMM_OK;
-    }
-    if (at.type == hipMemoryTypeManaged || at.type == hipMemoryTypeHost)
-        return MXGEMM_OK;
-    return fail(MXGEMM_EINVAL, "%s is not memory the GPU can access (host memory that is not "
-                "pinned?)", name);
-}
-
+// handle's device, managed memory or pinned host memory.  Checked whenever
+// the pointers differ from the last ones that passed (so a steady loop, and
+// graph capture after an eager run, make no extra calls).  Buffer sizes are
+// the caller's contract and are not checked: an allocation's range as the
+// runtime reports it need not be all of the memory mapped behind a pointer.
 int check_buffers(mxgemm_seg* h, const void* const (&ptr)[5])
 {
     static const char* const names[5] = {"a_seg", "a_scale", "b", "b_scale", "c"};
@@ -655,7 +655,7 @@ int64_t align256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
 extern "C" {
 
-const char* mxgemm_seg_last_error(void) { return g_err.c_str(); }
+const char* mxgemm_seg_last_error(void) { return mxg::g_err.c_str(); }
 
 int mxgemm_seg_plan(mxgemm_seg_plan_t* out, int64_t M, int64_t kPerRank, int32_t rank_size,
                     int64_t N, int64_t commMSize, int32_t buffer_count, int32_t num_cus,
