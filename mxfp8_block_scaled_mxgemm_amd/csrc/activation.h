@@ -14,24 +14,51 @@ __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float activate(int act, float z)
+__device__ __forceinline__ float relu(float z) { return z != z ? z : fmaxf(z, 0.f); }
+// The normal distribution function 0.5 (1 + erf(z / sqrt 2)), erf by
+// Abramowitz and Stegun's formula 7.1.26 (error below 1.5e-7), without the
+// branches of a full-precision erf: the epilogue is bound by instructions.
+// The tail is formed on the side where it is small, so nothing cancels there.
+__device__ __forceinline__ float normal_cdf(float z)
 {
-    switch (act) {
-    case kActRelu: return z != z ? z : fmaxf(z, 0.f);
-    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case kActGeluTanh: return z * sigmoid(kGeluC * (z + kGeluA * z * z * z));
-    case kActSilu: return z * sigmoid(z);
-    default: return z;
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+    const float poly =
+        t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float tail = 0.5f * poly * __expf(-x * x);
+    return z < 0.f ? tail : 1.f - tail;
+}
+__device__ __forceinline__ float gelu(float z) { return z * normal_cdf(z); }
+__device__ __forceinline__ float gelu_tanh(float z) { return z * sigmoid(kGeluC * z * (1.f + kGeluA * z * z)); }
+__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
+
+// act(z) of N values: one branch for all of them, eight at a time (the fence
+// keeps the scheduler from holding the temporaries of all of them at once).
+template <int N, class F>
+__device__ __forceinline__ void by_eights(float (&z)[N], const F& f)
+{
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+#pragma unroll
+        for (int u = k; u < k + 8 && u < N; ++u)
+            z[u] = f(z[u]);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-__device__ __forceinline__ void activate8(int act, float (&z)[8])
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&z)[N])
 {
     if (act == kActNone)
         return;
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-        z[u] = activate(act, z[u]);
+    if (act == kActSilu)
+        by_eights(z, silu);
+    else if (act == kActGeluTanh)
+        by_eights(z, gelu_tanh);
+    else if (act == kActRelu)
+        by_eights(z, relu);
+    else
+        by_eights(z, gelu);
 }
 
 // act(z) in y; returns act'(z) (relu: 0 at 0).
@@ -39,15 +66,15 @@ __device__ __forceinline__ float activate_grad(int act, float z, float& y)
 {
     switch (act) {
     case kActRelu:
-        y = z != z ? z : fmaxf(z, 0.f);
+        y = relu(z);
         return z > 0.f ? 1.f : 0.f;
     case kActGelu: {
-        const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+        const float cdf = normal_cdf(z);
         y = z * cdf;
         return cdf + z * 0.3989422804014327f * __expf(-0.5f * z * z);
     }
     case kActGeluTanh: {
-        const float s = sigmoid(kGeluC * (z + kGeluA * z * z * z));
+        const float s = sigmoid(kGeluC * z * (1.f + kGeluA * z * z));
         y = z * s;
         return s + z * s * (1.f - s) * kGeluC * (1.f + 3.f * kGeluA * z * z);
     }

@@ -103,14 +103,34 @@ __device__ __forceinline__ MxScale mx_scale(uint32_t amax_bits)
     return s;
 }
 
-// Codes of four elements of the block, first in the low byte.
+// Codes of four elements of the block, first in the low byte, by the
+// conversion instructions (round to nearest even, subnormal codes kept;
+// elements within the format's range after scaling, as they are, but for
+// infinities, which the clamp saturates).  Same codes as fp8_rne.
 template <int F>
 __device__ __forceinline__ uint32_t mx_codes(const MxScale& s, float a, float b, float c, float d)
 {
-    if (s.nan)
-        return 0x7F7F7F7Fu;
-    return fp8_rne<F>(ldexpf(a, -s.e)) | (fp8_rne<F>(ldexpf(b, -s.e)) << 8) | (fp8_rne<F>(ldexpf(c, -s.e)) << 16) |
-           (fp8_rne<F>(ldexpf(d, -s.e)) << 24);
+    constexpr float kMax = F == kE5M2 ? 57344.f : 448.f;
+    a = __builtin_amdgcn_fmed3f(ldexpf(a, -s.e), -kMax, kMax);
+    b = __builtin_amdgcn_fmed3f(ldexpf(b, -s.e), -kMax, kMax);
+    c = __builtin_amdgcn_fmed3f(ldexpf(c, -s.e), -kMax, kMax);
+    d = __builtin_amdgcn_fmed3f(ldexpf(d, -s.e), -kMax, kMax);
+    int w;
+    if constexpr (F == kE5M2) {
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+    } else {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    }
+    return s.nan ? 0x7F7F7F7Fu : (uint32_t)w;
+}
+
+// max of x over four consecutive lanes (all of them active).
+__device__ __forceinline__ uint32_t quad_max(uint32_t x)
+{
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));    // lanes 1, 0, 3, 2
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true)); // lanes 2, 3, 0, 1
 }
 
 }  // namespace mxg
