@@ -185,6 +185,16 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
                              uint8_t* qt, uint8_t* st, int64_t ld_qt, float* d_bias, void* workspace,
                              int64_t workspace_bytes, void* stream);
 
+/*
+ * Bytes transposed: dst [batch][cols][rows] from src [batch][rows][cols], row
+ * stride ld_src, matrix stride src_batch (bytes): codes or scales held with
+ * their inner axis strided, laid out for mxgemm_linear.  Any alignment.
+ * Errors: EINVAL, EUNSUPPORTED (more than 65535 matrices or tiles of 128
+ * rows), EHIP.
+ */
+int mxgemm_transpose_bytes(const void* src, int64_t ld_src, int64_t src_batch, int64_t rows, int64_t cols,
+                           int64_t batch, void* dst, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 from typing import NamedTuple, Optional
 
 from . import _lib
@@ -19,7 +20,7 @@ from ._lib import FMT_E4M3, FMT_E5M2, PRECISION_EXACT, PRECISION_NATIVE, check
 EXPORTED_MOE = [
     "mxgemm_sort_tokens", "mxgemm_sort_tokens_workspace", "mxgemm_dispatch_tokens",
     "mxgemm_dispatch_tokens_mx", "mxgemm_combine_tokens", "mxgemm_combine_tokens_backward",
-    "mxgemm_linear", "mxgemm_epilogue_backward",
+    "mxgemm_linear", "mxgemm_epilogue_backward", "mxgemm_transpose_bytes",
 ]
 
 GROUP_NONE, GROUP_ROWS, GROUP_INNER = 0, 1, 2
@@ -32,15 +33,8 @@ _PRECISION = {"exact": PRECISION_EXACT, "native": PRECISION_NATIVE, PRECISION_EX
 STEP = 128          # granule of a product's inner length and of k_offsets
 
 
-class LinearArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in
-                ("a", "a_scale", "w", "w_scale", "bias", "residual", "out", "out_scale", "z", "offsets")] + \
-               [(n, ctypes.c_int64) for n in
-                ("rows", "N", "K", "lda", "ld_a_scale", "ldw", "ld_w_scale", "w_group", "w_scale_group",
-                 "ld_residual", "ld_out", "out_group", "ld_out_scale", "ld_z")] + \
-               [(n, ctypes.c_int32) for n in
-                ("mode", "experts", "a_format", "w_format", "precision", "bias_type", "act", "gated", "out_type",
-                 "tile_cfg")]
+# mxgemm_linear_t: ten pointers, fourteen int64, ten int32, in the header's order
+LINEAR_ARGS = struct.Struct("10P14q10i")
 
 
 class TokenSort(NamedTuple):
@@ -78,9 +72,10 @@ def _load():
         lib.mxgemm_combine_tokens.argtypes = [vp, i64, i32, i64, i32, i64, vp, i32, vp, vp, vp, i64, vp, i64, vp]
         lib.mxgemm_combine_tokens_backward.argtypes = [vp, i64, vp, i64, i32, i64, i32, i64, vp, i32, vp, vp, vp,
                                                        i64, vp, vp]
-        lib.mxgemm_linear.argtypes = [ctypes.POINTER(LinearArgs), vp]
+        lib.mxgemm_linear.argtypes = [ctypes.c_char_p, vp]
         lib.mxgemm_epilogue_backward.argtypes = [vp, i32, i64, vp, i64, i64, i64, i32, i32, vp, vp, i32, i32, vp,
                                                  vp, vp, vp, i64, vp, vp, i64, vp]
+        lib.mxgemm_transpose_bytes.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp]
         for name in EXPORTED_MOE:
             getattr(lib, name).restype = ctypes.c_int
         lib.mxgemm_sort_tokens_workspace.restype = i64
@@ -115,9 +110,17 @@ def _on_stream(fn):
     return call
 
 
-def _stream(t):
+def _run(fn, device, *args):
+    """fn(*args, stream) on ``device`` and its current stream."""
     import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+    i = device.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc:
+        check(rc)
 
 
 def _rows_of(t, name, device=None, dtypes=None, shape=None):
@@ -129,20 +132,22 @@ def _rows_of(t, name, device=None, dtypes=None, shape=None):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype} is not one of {', '.join(map(str, dtypes))}")
-    if t.dim() < 2 or (shape is not None and tuple(t.shape) != shape):
+    have = t.shape
+    if len(have) < 2 or (shape is not None and have != shape):
         raise ValueError(f"{name}: expected shape {shape if shape is not None else '[rows, columns]'}, "
-                         f"got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+                         f"got {tuple(have)}")
+    stride = t.stride()
+    if stride[-1] != 1 and have[-1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
     # a stride that no element is reached by may be anything
-    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+    return stride[-2] if have[-2] > 1 else have[-1]
 
 
 def _plain(t, name, device, dtype, shape):
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.device != device:
         raise TypeError(f"{name}: expected a tensor on {device}")
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -190,9 +195,8 @@ def sort_tokens(expert_ids, num_experts: int) -> TokenSort:
     e4, n4 = _up(E1, 4), _up(n, 4)
     mem = torch.empty(2 * e4 + 2 * n4 + work // 4, dtype=torch.int32, device=ids.device)
     p = mem.data_ptr()
-    with torch.cuda.device(ids.device):
-        check(lib.mxgemm_sort_tokens(ids.data_ptr(), ids.element_size(), T, k, E1 - 1, p, p + 4 * e4, p + 8 * e4,
-                                     p + 8 * e4 + 4 * n4, p + 8 * e4 + 8 * n4, work, _stream(ids)))
+    _run(lib.mxgemm_sort_tokens, ids.device, ids.data_ptr(), ids.element_size(), T, k, E1 - 1, p, p + 4 * e4,
+         p + 8 * e4, p + 8 * e4 + 4 * n4, p + 8 * e4 + 8 * n4, work)
     row = 2 * e4
     return TokenSort(mem[:E1], mem[e4:e4 + E1], mem[row:row + n].view(T, k), mem[row + n4:row + n4 + n])
 
@@ -218,9 +222,8 @@ def dispatch_tokens(x, sort: TokenSort):
     T, H = x.shape
     off, E, row_of, T, k = _sort_args(sort, x.device, T)
     rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-    with torch.cuda.device(x.device):
-        check(_load().mxgemm_dispatch_tokens(x.data_ptr(), ld, _types()[x.dtype], T, k, H, off, E, row_of,
-                                             rows.data_ptr(), H, _stream(x)))
+    _run(_load().mxgemm_dispatch_tokens, x.device, x.data_ptr(), ld, _types()[x.dtype], T, k, H, off, E, row_of,
+         rows.data_ptr(), H)
     return rows
 
 
@@ -236,9 +239,8 @@ def dispatch_tokens_mx(x, sort: TokenSort, fmt="e4m3"):
     off, E, row_of, T, k = _sort_args(sort, x.device, T)
     q = torch.empty((T * k, H), dtype=torch.uint8, device=x.device)
     s = torch.empty((T * k, H // 32), dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        check(_load().mxgemm_dispatch_tokens_mx(x.data_ptr(), ld, _types()[x.dtype], T, k, H, off, E, row_of,
-                                                q.data_ptr(), s.data_ptr(), _format(fmt), _stream(x)))
+    _run(_load().mxgemm_dispatch_tokens_mx, x.device, x.data_ptr(), ld, _types()[x.dtype], T, k, H, off, E, row_of,
+         q.data_ptr(), s.data_ptr(), _format(fmt))
     return q, s
 
 
@@ -256,10 +258,8 @@ def combine_tokens(rows, sort: TokenSort, weights=None, residual=None):
     w = None if weights is None else _plain(weights, "weights", rows.device, torch.float32, (T, k))
     ld_res = 0 if residual is None else _rows_of(residual, "residual", rows.device, (rows.dtype,), (T, H))
     out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
-    with torch.cuda.device(rows.device):
-        check(_load().mxgemm_combine_tokens(rows.data_ptr(), ld, _types()[rows.dtype], T, k, H, off, E, row_of, w,
-                                            None if residual is None else residual.data_ptr(), ld_res,
-                                            out.data_ptr(), H, _stream(rows)))
+    _run(_load().mxgemm_combine_tokens, rows.device, rows.data_ptr(), ld, _types()[rows.dtype], T, k, H, off, E,
+         row_of, w, None if residual is None else residual.data_ptr(), ld_res, out.data_ptr(), H)
     return out
 
 
@@ -282,19 +282,33 @@ def combine_tokens_backward(d_out, rows, sort: TokenSort, weights=None):
     w = None if weights is None else _plain(weights, "weights", rows.device, torch.float32, (T, k))
     d_rows = torch.empty((n, H), dtype=rows.dtype, device=rows.device)
     d_w = torch.empty((T, k), dtype=torch.float32, device=rows.device)
-    with torch.cuda.device(rows.device):
-        check(_load().mxgemm_combine_tokens_backward(d_out.data_ptr(), ld_d, rows.data_ptr(), ld,
-                                                     _types()[rows.dtype], T, k, H, off, E, row_of, w,
-                                                     d_rows.data_ptr(), H, d_w.data_ptr(), _stream(rows)))
+    _run(_load().mxgemm_combine_tokens_backward, rows.device, d_out.data_ptr(), ld_d, rows.data_ptr(), ld,
+         _types()[rows.dtype], T, k, H, off, E, row_of, w, d_rows.data_ptr(), H, d_w.data_ptr())
     return d_rows, d_w
 
 
 # ----------------------------------------------------------------- product --
 
+def _laid_out(t):
+    """``t``, or where its other axis is the contiguous one (a transposed view)
+    a copy with contiguous rows; [.., N, K] bytes."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8 or not 2 <= t.dim() <= 3:
+        return t            # refused by the checks that follow
+    stride, shape = t.stride(), t.shape
+    if stride[-1] == 1 or shape[-1] <= 1 or stride[-2] != 1 or stride[-1] < shape[-2]:
+        return t
+    out = torch.empty(shape, dtype=torch.uint8, device=t.device)
+    _run(_load().mxgemm_transpose_bytes, t.device, t.data_ptr(), stride[-1], stride[0] if len(shape) == 3 else 0,
+         shape[-1], shape[-2], shape[0] if len(shape) == 3 else 1, out.data_ptr())
+    return out
+
+
 def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, out_dtype, preact, precision, a_fmt,
             w_fmt, tile_cfg):
     import torch
     u8 = (torch.uint8,)
+    a, a_scale, w, w_scale = _laid_out(a), _laid_out(a_scale), _laid_out(w), _laid_out(w_scale)
     lda = _rows_of(a, "a", dtypes=u8)
     dev = a.device
     if a.dim() != 2:
@@ -309,8 +323,7 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         raise ValueError(f"w: expected {'[experts, N, K]' if by_row else '[N, K]'} with K = {K}, got {tuple(w.shape)}")
     N = w.shape[-2]
     ldw_s = _rows_of(w_scale, "w_scale", dev, u8, (*w.shape[:-1], K // 32))
-    E = 0
-    off = None
+    E = off = 0
     if mode != GROUP_NONE:
         E = w.shape[0] if by_row else offsets.shape[0] - 1
         off = _plain(offsets, "offsets", dev, torch.int32, (E + 1,))
@@ -322,39 +335,34 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         raise ValueError(f"out_dtype {out_dtype!r} is not a 16- or 32-bit float type, 'e4m3' or 'e5m2'")
     if mx and cols % 32:
         raise ValueError(f"MXFP8 output needs columns in blocks of 32, not {cols}")
-    kind = torch.uint8 if mx else out_dtype
-    g = LinearArgs(a=a.data_ptr(), a_scale=a_scale.data_ptr(), w=w.data_ptr(), w_scale=w_scale.data_ptr(),
-                   offsets=off, rows=M, N=N, K=K, lda=lda, ld_a_scale=lda_s, ldw=ldw, ld_w_scale=ldw_s, mode=mode,
-                   experts=E, a_format=_format(a_fmt), w_format=_format(w_fmt), act=_activation(act),
-                   gated=1 if gated else 0, out_type=_MX_OUT[out_dtype] if mx else _types()[out_dtype],
-                   tile_cfg=tile_cfg, ld_out=cols)
     if precision not in _PRECISION:
         raise ValueError(f"unknown precision mode {precision!r}")
-    g.precision = _PRECISION[precision]
-    if by_row:
-        g.w_group, g.w_scale_group = w.stride(0), w_scale.stride(0)
+    bias_ptr = res_ptr = scale_ptr = z_ptr = ld_res = bias_type = 0
     if bias is not None:
         if bias.dtype not in _types():
             raise TypeError(f"bias: {bias.dtype} is not a 16- or 32-bit float type")
-        g.bias = _plain(bias, "bias", dev, bias.dtype, (E, N) if by_row else (N,))
-        g.bias_type = _types()[bias.dtype]
+        bias_ptr = _plain(bias, "bias", dev, bias.dtype, (E, N) if by_row else (N,))
+        bias_type = _types()[bias.dtype]
     if residual is not None:
-        g.ld_residual = _rows_of(residual, "residual", dev, (torch.bfloat16 if mx else out_dtype,), (M, cols))
-        g.residual = residual.data_ptr()
-    out = torch.empty((E, M, cols) if mode == GROUP_INNER else (M, cols), dtype=kind, device=dev)
-    g.out = out.data_ptr()
-    g.out_group = M * cols
+        ld_res = _rows_of(residual, "residual", dev, (torch.bfloat16 if mx else out_dtype,), (M, cols))
+        res_ptr = residual.data_ptr()
+    out = torch.empty((E, M, cols) if mode == GROUP_INNER else (M, cols), dtype=torch.uint8 if mx else out_dtype,
+                      device=dev)
     result = [out]
     if mx:
         scale = torch.empty((M, cols // 32), dtype=torch.uint8, device=dev)
-        g.out_scale, g.ld_out_scale = scale.data_ptr(), cols // 32
+        scale_ptr = scale.data_ptr()
         result.append(scale)
     if preact:
         z = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        g.z, g.ld_z = z.data_ptr(), N
+        z_ptr = z.data_ptr()
         result.append(z)
-    with torch.cuda.device(dev):
-        check(_load().mxgemm_linear(ctypes.byref(g), _stream(a)))
+    w_group, w_scale_group = (w.stride(0), w_scale.stride(0)) if by_row else (0, 0)
+    _run(_load().mxgemm_linear, dev, LINEAR_ARGS.pack(
+        a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias_ptr, res_ptr, out.data_ptr(),
+        scale_ptr, z_ptr, off, M, N, K, lda, lda_s, ldw, ldw_s, w_group, w_scale_group, ld_res, cols, M * cols,
+        cols // 32, N, mode, E, _format(a_fmt), _format(w_fmt), _PRECISION[precision], bias_type, _activation(act),
+        1 if gated else 0, _MX_OUT[out_dtype] if mx else _types()[out_dtype], tile_cfg))
     return result[0] if len(result) == 1 else tuple(result)
 
 
@@ -365,7 +373,8 @@ def linear(a, a_scale, w, w_scale, bias=None, act="none", gated=False, residual=
     z[:, N/2:] + residual.
 
     a [M, K], w [N, K]: MXFP8 codes (uint8, K a multiple of 128) with scales
-    [.., K / 32].  With ``offsets`` (TokenSort.offsets) w is [E, N, K], bias
+    [.., K / 32]; transposed views (K strided, the other axis contiguous) are
+    first copied into that layout.  With ``offsets`` (TokenSort.offsets) w is [E, N, K], bias
     [E, N], and rows offsets[e] .. offsets[e + 1] of a meet expert e's; rows
     of no expert give zeros.  act: none, relu, gelu, gelu_tanh, silu.
     out_dtype: bfloat16 (default), float16, float32, or "e4m3" / "e5m2" for
@@ -416,11 +425,9 @@ def _epilogue_backward(d_out, z, act, gated, sort, fmt, rows, cols, bias):
         db = torch.empty((E, N) if E else (N,), dtype=torch.float32, device=dev)
         work = torch.empty((ld_qt // STEP, N), dtype=torch.float32, device=dev)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    with torch.cuda.device(dev):
-        check(_load().mxgemm_epilogue_backward(
-            d_out.data_ptr(), _types()[d_out.dtype], ld_d, ptr(z), ld_z, M, N, _activation(act), 1 if gated else 0,
-            off or None, koff or None, E, _format(fmt), ptr(q), ptr(s), ptr(qt), ptr(st), ld_qt, ptr(db), ptr(work),
-            0 if work is None else work.numel() * 4, _stream(d_out)))
+    _run(_load().mxgemm_epilogue_backward, dev, d_out.data_ptr(), _types()[d_out.dtype], ld_d, ptr(z), ld_z, M, N,
+         _activation(act), 1 if gated else 0, off or None, koff or None, E, _format(fmt), ptr(q), ptr(s), ptr(qt),
+         ptr(st), ld_qt, ptr(db), ptr(work), 0 if work is None else work.numel() * 4)
     return (q, s), (qt, st), db
 
 

@@ -91,4 +91,13 @@ struct GradArgs {
 };
 hipError_t launch_grad(const GradArgs& a, hipStream_t stream);
 
+// dst[batch][cols][rows] = src[batch][rows][cols] transposed, bytes.
+struct TransposeArgs {
+    const uint8_t* src;
+    int64_t src_batch, ld_src;
+    uint8_t* dst;
+    int64_t rows, cols, batch;
+};
+hipError_t launch_transpose(const TransposeArgs& a, hipStream_t stream);
+
 }  // namespace mxg

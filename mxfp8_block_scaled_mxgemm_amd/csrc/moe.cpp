@@ -583,4 +583,24 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
     return MXGEMM_OK;
 }
 
+int mxgemm_transpose_bytes(const void* src, int64_t ld_src, int64_t src_batch, int64_t rows, int64_t cols,
+                           int64_t batch, void* dst, void* stream)
+{
+    if (rows < 0 || cols < 0 || batch < 0)
+        return fail(MXGEMM_EINVAL, "sizes must not be negative");
+    TRY(check_stride("src", ld_src, cols));
+    if (batch > 65535 || rows > 65535LL * 128 || cols > (1LL << 31))
+        return fail(MXGEMM_EUNSUPPORTED, "%lld matrices of %lld x %lld bytes are too many", (long long)batch,
+                    (long long)rows, (long long)cols);
+    if (rows == 0 || cols == 0 || batch == 0)
+        return MXGEMM_OK;
+    int dev, cus;
+    TRY(current_device(&dev, &cus));
+    const Buffer bufs[] = {{src, "src", 1, false}, {dst, "dst", 1, false}};
+    TRY(check_buffers(bufs, dev));
+    const mxg::TransposeArgs a = {(const uint8_t*)src, src_batch, ld_src, (uint8_t*)dst, rows, cols, batch};
+    HIP_TRY(mxg::launch_transpose(a, (hipStream_t)stream));
+    return MXGEMM_OK;
+}
+
 }  // extern "C"
