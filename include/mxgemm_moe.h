@@ -150,8 +150,16 @@ typedef struct mxgemm_linear {
     int32_t a_format, w_format;   /* MXGEMM_FMT_*       */
     int32_t precision;            /* MXGEMM_PRECISION_* */
     int32_t bias_type, act, gated, out_type;
-    int32_t tile_cfg;             /* -1: chosen by the sizes (tests force one, 0 .. 6) */
+    int32_t tile_cfg;             /* -1: chosen by the sizes (tests force one, 0 .. 5) */
+    void* workspace;              /* 16-byte aligned, or NULL                          */
+    int64_t workspace_bytes;
 } mxgemm_linear_t;
+
+/* Bytes of workspace with which a product of these sizes that is not by
+ * expert may split K over work-groups (their FP32 sums are added in order by
+ * a second launch); 0 where it would not.  Without a workspace, or with a
+ * smaller one, the product is formed unsplit. */
+int64_t mxgemm_linear_workspace(int64_t rows, int64_t N, int64_t K);
 
 int mxgemm_linear(const mxgemm_linear_t* args, void* stream);
 

@@ -20,7 +20,7 @@ from ._lib import FMT_E4M3, FMT_E5M2, PRECISION_EXACT, PRECISION_NATIVE, check
 EXPORTED_MOE = [
     "mxgemm_sort_tokens", "mxgemm_sort_tokens_workspace", "mxgemm_dispatch_tokens",
     "mxgemm_dispatch_tokens_mx", "mxgemm_combine_tokens", "mxgemm_combine_tokens_backward",
-    "mxgemm_linear", "mxgemm_epilogue_backward", "mxgemm_transpose_bytes",
+    "mxgemm_linear", "mxgemm_linear_workspace", "mxgemm_epilogue_backward", "mxgemm_transpose_bytes",
 ]
 
 GROUP_NONE, GROUP_ROWS, GROUP_INNER = 0, 1, 2
@@ -33,8 +33,9 @@ _PRECISION = {"exact": PRECISION_EXACT, "native": PRECISION_NATIVE, PRECISION_EX
 STEP = 128          # granule of a product's inner length and of k_offsets
 
 
-# mxgemm_linear_t: ten pointers, fourteen int64, ten int32, in the header's order
-LINEAR_ARGS = struct.Struct("10P14q10i")
+# mxgemm_linear_t: ten pointers, fourteen int64, ten int32, the workspace, in
+# the header's order
+LINEAR_ARGS = struct.Struct("10P14q10iPq")
 
 
 class TokenSort(NamedTuple):
@@ -78,7 +79,8 @@ def _load():
         lib.mxgemm_transpose_bytes.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp]
         for name in EXPORTED_MOE:
             getattr(lib, name).restype = ctypes.c_int
-        lib.mxgemm_sort_tokens_workspace.restype = i64
+        lib.mxgemm_linear_workspace.argtypes = [i64, i64, i64]
+        lib.mxgemm_sort_tokens_workspace.restype = lib.mxgemm_linear_workspace.restype = i64
         _bound = lib
     return _bound
 
@@ -357,12 +359,18 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         z = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         z_ptr = z.data_ptr()
         result.append(z)
+    work_ptr = work = 0
+    # mxgemm_linear_workspace's rule
+    if mode == GROUP_NONE and M > 32 and K >= 2048 and -(-M // 64) * -(-N // 64) <= 128:
+        work = 4 << 20
+        work_mem = torch.empty(work, dtype=torch.uint8, device=dev)
+        work_ptr = work_mem.data_ptr()
     w_group, w_scale_group = (w.stride(0), w_scale.stride(0)) if by_row else (0, 0)
     _run(_load().mxgemm_linear, dev, LINEAR_ARGS.pack(
         a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias_ptr, res_ptr, out.data_ptr(),
         scale_ptr, z_ptr, off, M, N, K, lda, lda_s, ldw, ldw_s, w_group, w_scale_group, ld_res, cols, M * cols,
         cols // 32, N, mode, E, _format(a_fmt), _format(w_fmt), _PRECISION[precision], bias_type, _activation(act),
-        1 if gated else 0, _MX_OUT[out_dtype] if mx else _types()[out_dtype], tile_cfg))
+        1 if gated else 0, _MX_OUT[out_dtype] if mx else _types()[out_dtype], tile_cfg, work_ptr, work))
     return result[0] if len(result) == 1 else tuple(result)
 
 

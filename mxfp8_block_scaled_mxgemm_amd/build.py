@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libmxgemm_seg.so")
 # One GEMM (and one fused-product) translation unit per pair of FP8 formats,
 # compiled in parallel.
 SOURCES = ["kernels.hip", "gemm_e4m3_e4m3.hip", "gemm_e5m2_e5m2.hip", "gemm_e4m3_e5m2.hip",
-           "gemm_e5m2_e4m3.hip", "ring.hip", "mxgemm_seg.cpp", "tokens.hip", "grad.hip", "layout.hip",
+           "gemm_e5m2_e4m3.hip", "ring.hip", "mxgemm_seg.cpp", "tokens.hip", "grad.hip", "layout.hip", "linear_finish.hip",
            "linear_e4m3_e4m3.hip", "linear_e5m2_e5m2.hip", "linear_e4m3_e5m2.hip",
            "linear_e5m2_e4m3.hip", "moe.cpp"]
 ARCH = "gfx950"

@@ -43,6 +43,9 @@ struct LinArgs {
     uint16_t* z;                  // bfloat16 [rows][N] or null: z, before the activation
     int64_t ld_z;
     // plan
+    int skinny;                   // kSkinny*, for the skinny tiles
+    int split;                    // K splits (kLin64x64, kDense), their sums in `part`
+    float* part;                  // [split][rows][N]
     int tiles_m, tiles_n, group_n, total_work;
 };
 
@@ -52,18 +55,23 @@ enum {
     kLin256x128 = 1,
     kLin128x128 = 2,
     kLin64x64 = 3,                // four K groups
-    kLinRows64 = 4,               // 64, 32 or 16 rows, weights straight to registers
-    kLinRows32 = 5,
-    kLinRows16 = 6,
-    kLinCfgs = 7
+    kLinRows32 = 4,               // 32 or 16 rows, weights straight to registers
+    kLinRows16 = 5,
+    kLinCfgs = 6
 };
+
+// Skinny tiles: 16 columns and sixteen waves; 32 columns and 2, 4 or 8 waves;
+// 64 columns of a gated product with MXFP8 output (32 outputs: its block)
+enum { kSkinnyNarrow, kSkinny2, kSkinny4, kSkinny8, kSkinnyWide };
 
 struct LinTile {
     int tile_m, tile_n;           // tile_n: columns of the product
 };
 
 hipError_t launch_linear(int cfg, bool exact, int fa, int fw, const LinArgs& a, hipStream_t stream);
-// Columns of the product per tile of configuration cfg.
+// Sums of a product with split > 1 through its epilogue.
+hipError_t launch_linear_finish(const LinArgs& a, hipStream_t stream);
+// Tile of configuration cfg.
 LinTile lin_tile(int cfg, const LinArgs& a);
 
 // Gradient of the epilogue, in tiles of 128 tokens x 64 columns of the

@@ -27,28 +27,37 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
 // [k0, k0 + steps).  zero: rows that belong to no expert.
 struct LinItem {
     int m0, end, tn, e, k0, steps;
+    int ks;             // K split
     bool zero;
 };
 
 // Row tile tm of the list of all experts' row tiles: expert e has
 // ceil(rows of e / BM) of them, and the rows past the last expert come as one
-// expert more.  All 64 lanes of the wave take part; the offsets are clamped
-// to the rows there are.  False past the end of the list.
+// expert more.  All 64 lanes of the wave take part, four experts each, so up
+// to 255 experts take one round of loads; the offsets are clamped to the rows
+// there are.  False past the end of the list.
 template <int BM>
 __device__ __forceinline__ bool find_rows(const LinArgs& p, int tm, int lane, LinItem& it)
 {
     int before = 0;
-    for (int g0 = 0; g0 <= p.groups; g0 += 64) {
-        const int g = g0 + lane;
-        int lo = 0, hi = 0;
-        if (g <= p.groups) {
-            lo = p.offsets[g];
-            hi = g < p.groups ? p.offsets[g + 1] : p.rows;
-            lo = lo < 0 ? 0 : lo > p.rows ? p.rows : lo;
-            hi = hi < lo ? lo : hi > p.rows ? p.rows : hi;
+    for (int g0 = 0; g0 <= p.groups; g0 += 256) {
+        int at[5], n[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int g = g0 + 4 * lane + i;
+            at[i] = g <= p.groups ? p.offsets[g] : p.rows;
         }
-        const int n = (hi - lo + BM - 1) / BM;
-        int inc = n;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int lo = i ? at[i - 1] : 0;
+            at[i] = at[i] < lo ? lo : at[i] > p.rows ? p.rows : at[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            n[i] = (at[i + 1] - at[i] + BM - 1) / BM;
+            sum += n[i];
+        }
+        int inc = sum;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int x = __shfl_up(inc, d);
@@ -57,9 +66,17 @@ __device__ __forceinline__ bool find_rows(const LinArgs& p, int tm, int lane, Li
         const uint64_t past = __ballot(before + inc > tm);
         if (past) {
             const int l = __builtin_ctzll(past);
-            const int first = before + __shfl(inc - n, l);
-            it.e = __builtin_amdgcn_readfirstlane(g0 + l);
-            it.m0 = __builtin_amdgcn_readfirstlane(__shfl(lo, l) + (tm - first) * BM);
+            int first = before + inc - sum, lo = at[0], hi = at[1], e = g0 + 4 * lane;
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                if (tm >= first + n[i - 1] && e == g0 + 4 * lane + i - 1) {
+                    first += n[i - 1];
+                    lo = at[i];
+                    hi = at[i + 1];
+                    ++e;
+                }
+            it.e = __builtin_amdgcn_readfirstlane(__shfl(e, l));
+            it.m0 = __builtin_amdgcn_readfirstlane(__shfl(lo + (tm - first) * BM, l));
             it.end = __builtin_amdgcn_readfirstlane(__shfl(hi, l));
             it.zero = it.e == p.groups;
             return true;
@@ -89,9 +106,15 @@ __device__ __forceinline__ bool lin_item(const LinArgs& p, int lane, LinItem& it
         it.k0 = lo / kBK;
         it.steps = hi / kBK - it.k0;
     }
-    const TileCoord tc = decode_work(rest, p.tiles_m, p.tiles_n, 1, p.group_n);
+    const TileCoord tc = decode_work(rest, p.tiles_m, p.tiles_n, p.split, p.group_n);
     it.tn = tc.tn;
     it.m0 = tc.tm * BM;
+    it.ks = tc.ks;
+    if (p.split > 1) {      // K-steps in even runs, the first ones a step longer
+        const int share = it.steps / p.split, more = it.steps % p.split;
+        it.k0 = tc.ks * share + (tc.ks < more ? tc.ks : more);
+        it.steps = share + (tc.ks < more ? 1 : 0);
+    }
     if (p.mode == kByRows)
         return find_rows<BM>(p, tc.tm, lane, it);
     return true;
@@ -823,6 +846,41 @@ __device__ __forceinline__ void groups_epilogue(const LinArgs& p, uint8_t* lds, 
                                    it.e, wave * kRows, kRows, lane);
 }
 
+// The same with K split over work-groups: the sums go to the workspace,
+// [split][rows][N] in FP32, gated columns still in the product's order.
+template <int WGK>
+__device__ __forceinline__ void groups_partial(const LinArgs& p, uint8_t* lds, v16f (&acc)[2][2], const LinItem& it,
+                                               int n0, int wave, int lane)
+{
+    constexpr int kRows = 32 / WGK;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        slab_write<2>(lds + (i * WGK + wave) * kSlabBytes, acc[i], 0, lane);
+    __syncthreads();
+    const int c8 = lane & 7;
+    // gated tiles hold 32 gate columns, then 32 up columns
+    const int half = p.N / 2;
+    const int c = !p.gated ? n0 + 8 * c8 : n0 / 2 + 8 * (c8 & 3);
+    const int n = !p.gated ? p.N : half;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = wave * kRows + (lane >> 3), row = it.m0 + 32 * i + r;
+        float z[8];
+        slab_read8<WGK, 0>(lds + i * WGK * kSlabBytes, r, c8, z);
+        if (row >= it.end)
+            continue;
+        float* out = p.part + ((int64_t)it.ks * p.rows + row) * p.N + c + (p.gated && c8 >= 4 ? half : 0);
+        if (c + 8 <= n) {
+            __builtin_memcpy(out, z, 32);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u < n)
+                    out[u] = z[u];
+        }
+    }
+}
+
 // One BM x BN tile of the product per work-group, WGK K groups of WGM x WGN
 // waves (each a run of the K-steps; a group whose steps run out one early
 // only meets the last barrier).  After the K loop the stages are
@@ -903,7 +961,9 @@ linear_kernel(LinArgs p)
     __syncthreads();        // every wave has read its last fragments
     if constexpr (WGK > 1) {
         static_assert(NWG == 1 && GA == 2 && GB == 2 && 2 * WGK * kSlabBytes <= kLds, "two sets of slabs");
-        if (p.gated)
+        if (p.split > 1)
+            groups_partial<WGK>(p, lds, acc, it, n0, wave, lane);
+        else if (p.gated)
             groups_epilogue<true, WGK>(p, lds, acc, it, n0, cols, wave, lane);
         else
             groups_epilogue<false, WGK>(p, lds, acc, it, n0, cols, wave, lane);
@@ -978,8 +1038,8 @@ __device__ __forceinline__ void skinny_epilogue(const LinArgs& p, const float* r
 // MFMA's operand layout (lane l: row l % 16, K [16 q, +16) and [64 + 16 q,
 // +16), q = l / 16), without LDS.  A work-group of NW waves takes NB blocks
 // of 16 columns (gated: the first NB / 2 gate, the others up) and splits K
-// over its waves in runs of K-steps; U steps' loads are in flight per wave
-// before the first is multiplied.  The waves' sums are added in wave order
+// over its waves in runs of K-steps; the loads of U steps are in flight per
+// wave.  The waves' sums are added in wave order
 // through LDS, where the epilogue reads them row-wise.
 template <int RT, int NB, int NW, int U, bool EXACT, int FA, int FB>
 __global__ void __launch_bounds__(NW * 64) linear_skinny_kernel(LinArgs p)
@@ -1028,80 +1088,103 @@ __global__ void __launch_bounds__(NW * 64) linear_skinny_kernel(LinArgs p)
 
     const int per = (it.steps + NW - 1) / NW;
     const int lo = wave * per, hi = lo + per < it.steps ? lo + per : it.steps;
-    for (int s0 = lo; s0 < hi; s0 += U) {
-        u32x4 wv[U][NB][2], av[U][RT][2];
-        uint32_t wsv[U][NB], asv[U][RT];
+    u32x4 wv[U][NB][2], av[U][RT][2];
+    uint32_t wsv[U][NB], asv[U][RT];
+    auto load = [&](auto uc, int s) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u < hi ? s0 + u : hi - 1;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                wv[u][b][0] = *reinterpret_cast<const u32x4*>(wp[b] + (int64_t)s * kBK);
-                wv[u][b][1] = *reinterpret_cast<const u32x4*>(wp[b] + (int64_t)s * kBK + 64);
-                wsv[u][b] = *reinterpret_cast<const uint32_t*>(wsp[b] + (int64_t)s * 4);
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                av[u][r][0] = *reinterpret_cast<const u32x4*>(ap[r] + (int64_t)s * kBK);
-                av[u][r][1] = *reinterpret_cast<const u32x4*>(ap[r] + (int64_t)s * kBK + 64);
-                asv[u][r] = *reinterpret_cast<const uint32_t*>(asp[r] + (int64_t)s * 4);
-            }
+        for (int b = 0; b < NB; ++b) {
+            wv[u][b][0] = *reinterpret_cast<const u32x4*>(wp[b] + (int64_t)s * kBK);
+            wv[u][b][1] = *reinterpret_cast<const u32x4*>(wp[b] + (int64_t)s * kBK + 64);
+            wsv[u][b] = *reinterpret_cast<const uint32_t*>(wsp[b] + (int64_t)s * 4);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s0 + u >= hi)
-                break;
-            if constexpr (EXACT) {
-                // as in mxgemm_kernel's 16-wide exact form: half h of the
-                // step is the lane's chunk h, scaled by MX block 2 h + q / 2
-                const int shift = 8 * (lq >> 1);
+        for (int r = 0; r < RT; ++r) {
+            av[u][r][0] = *reinterpret_cast<const u32x4*>(ap[r] + (int64_t)s * kBK);
+            av[u][r][1] = *reinterpret_cast<const u32x4*>(ap[r] + (int64_t)s * kBK + 64);
+            asv[u][r] = *reinterpret_cast<const uint32_t*>(asp[r] + (int64_t)s * 4);
+        }
+    };
+    auto multiply = [&](auto uc, int s) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        __builtin_amdgcn_sched_barrier(0);      // one step's conversions at a time
+        if constexpr (EXACT) {
+            // as in mxgemm_kernel's 16-wide exact form: half h of the
+            // step is the lane's chunk h, scaled by MX block 2 h + q / 2
+            const int shift = 8 * (lq >> 1);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        v8bf bb[NB], ab[RT];
+                for (int m = 0; m < 2; ++m) {
+                    v8bf bb[NB], ab[RT];
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const u32x4 x = wv[u][b][h];
-                            bb[b] = fp8x8_to_bf16<FB>(m ? u32x2{x.z, x.w} : u32x2{x.x, x.y},
-                                                      e8m0_to_f32(wsv[u][b] >> (shift + 16 * h)));
-                        }
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const u32x4 x = av[u][r][h];
-                            ab[r] = fp8x8_to_bf16<FA>(m ? u32x2{x.z, x.w} : u32x2{x.x, x.y},
-                                                      e8m0_to_f32(asv[u][r] >> (shift + 16 * h)));
-                        }
-#pragma unroll
-                        for (int r = 0; r < RT; ++r)
-#pragma unroll
-                            for (int b = 0; b < NB; ++b)
-                                acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bb[b], ab[r], acc[r][b], 0, 0, 0);
+                    for (int b = 0; b < NB; ++b) {
+                        const u32x4 x = wv[u][b][h];
+                        bb[b] = fp8x8_to_bf16<FB>(m ? u32x2{x.z, x.w} : u32x2{x.x, x.y},
+                                                  e8m0_to_f32(wsv[u][b] >> (shift + 16 * h)));
                     }
-                // fresh sums per pair of K-steps, as in the other exact forms
-                if (((s0 + u - lo) & 1) == 1 || s0 + u == hi - 1) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const u32x4 x = av[u][r][h];
+                        ab[r] = fp8x8_to_bf16<FA>(m ? u32x2{x.z, x.w} : u32x2{x.x, x.y},
+                                                  e8m0_to_f32(asv[u][r] >> (shift + 16 * h)));
+                    }
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            tot[r][b] += acc[r][b];
-                            acc[r][b] = v4f{0.f, 0.f, 0.f, 0.f};
-                        }
+                        for (int b = 0; b < NB; ++b)
+                            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bb[b], ab[r], acc[r][b], 0, 0, 0);
                 }
-            } else {
+            // fresh sums per pair of K-steps, as in the other exact forms
+            if (((s - lo) & 1) == 1 || s == hi - 1) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        const u32x4 x0 = wv[u][b][0], x1 = wv[u][b][1], y0 = av[u][r][0], y1 = av[u][r][1];
-                        tot[r][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            v8i{(int)x0.x, (int)x0.y, (int)x0.z, (int)x0.w, (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w},
-                            v8i{(int)y0.x, (int)y0.y, (int)y0.z, (int)y0.w, (int)y1.x, (int)y1.y, (int)y1.z, (int)y1.w},
-                            tot[r][b], FB, FA, 0, (int)(wsv[u][b] >> (8 * lq)), 0, (int)(asv[u][r] >> (8 * lq)));
+                        tot[r][b] += acc[r][b];
+                        acc[r][b] = v4f{0.f, 0.f, 0.f, 0.f};
                     }
             }
+        } else {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const u32x4 x0 = wv[u][b][0], x1 = wv[u][b][1], y0 = av[u][r][0], y1 = av[u][r][1];
+                    tot[r][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        v8i{(int)x0.x, (int)x0.y, (int)x0.z, (int)x0.w, (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w},
+                        v8i{(int)y0.x, (int)y0.y, (int)y0.z, (int)y0.w, (int)y1.x, (int)y1.y, (int)y1.z, (int)y1.w},
+                        tot[r][b], FB, FA, 0, (int)(wsv[u][b] >> (8 * lq)), 0, (int)(asv[u][r] >> (8 * lq)));
+                }
         }
-    }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // The loads of U steps are always on their way: a step's registers are
+    // loaded again, U steps on, as soon as it is multiplied.
+    static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+        if (lo + decltype(uc)::value < hi)
+            load(uc, lo + decltype(uc)::value);
+    });
+    int s0 = lo;
+    for (; s0 + 2 * U <= hi; s0 += U)
+        static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value;
+            multiply(uc, s0 + u);
+            load(uc, s0 + u + U);
+        });
+    static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        if (s0 + u < hi) {
+            multiply(uc, s0 + u);
+            if (s0 + u + U < hi)
+                load(uc, s0 + u + U);
+        }
+    });
+    static_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        if (s0 + u + U < hi)
+            multiply(uc, s0 + u + U);
+    });
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -1145,25 +1228,33 @@ static hipError_t launch_lin_skinny(bool exact, const LinArgs& a, hipStream_t st
     return hipGetLastError();
 }
 
-// Blocks of 16 columns of a skinny tile (see lin_tile).
+// Skinny tiles: blocks of 16 columns per tile and waves per work-group by the
+// plan's choice.  Measured (exact): experts' 2048 x 768 weights, 64 pairs over
+// 128 experts, 22 / 26 / 39 us with 2 / 4 / 8 waves; 4096 x 4096 weights, 512
+// pairs over 64, 373 / 357 / 362 us; one row x 8192 x 8192, 20.7 / 16.6 / 16.0 us.
+template <int RT, int FA, int FB>
+static hipError_t launch_lin_rows(bool exact, const LinArgs& a, hipStream_t stream)
+{
+    switch (a.skinny) {
+    case kSkinnyNarrow: return launch_lin_skinny<RT, 1, 16, 2, FA, FB>(exact, a, stream);
+    case kSkinny2: return launch_lin_skinny<RT, 2, 2, 2, FA, FB>(exact, a, stream);
+    case kSkinny4: return launch_lin_skinny<RT, 2, 4, 2, FA, FB>(exact, a, stream);
+    case kSkinny8: return launch_lin_skinny<RT, 2, 8, 2, FA, FB>(exact, a, stream);
+    case kSkinnyWide: return launch_lin_skinny<RT, 4, 4, 1, FA, FB>(exact, a, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
 template <int FA, int FB>
 hipError_t launch_linear_fmt(int cfg, bool exact, const LinArgs& a, hipStream_t stream)
 {
-    const int nb = lin_tile(cfg, a).tile_n / 16;
     switch (cfg) {
     case kLin256x256: return launch_lin_tile<256, 256, 2, 2, 2, 2, 1, FA, FB>(exact, a, stream);
     case kLin256x128: return launch_lin_tile<256, 128, 2, 2, 4, 2, 1, FA, FB>(exact, a, stream);
     case kLin128x128: return launch_lin_tile<128, 128, 2, 2, 2, 2, 1, FA, FB>(exact, a, stream);
     case kLin64x64: return launch_lin_tile<64, 64, 1, 1, 1, 1, 4, FA, FB>(exact, a, stream);
-    case kLinRows64:
-        return nb == 4 ? launch_lin_skinny<4, 4, 8, 1, FA, FB>(exact, a, stream)
-                       : launch_lin_skinny<4, 2, 8, 2, FA, FB>(exact, a, stream);
-    case kLinRows32:
-        return nb == 4 ? launch_lin_skinny<2, 4, 8, 2, FA, FB>(exact, a, stream)
-                       : launch_lin_skinny<2, 2, 8, 4, FA, FB>(exact, a, stream);
-    case kLinRows16:
-        return nb == 4 ? launch_lin_skinny<1, 4, 8, 4, FA, FB>(exact, a, stream)
-                       : launch_lin_skinny<1, 2, 8, 4, FA, FB>(exact, a, stream);
+    case kLinRows32: return launch_lin_rows<2, FA, FB>(exact, a, stream);
+    case kLinRows16: return launch_lin_rows<1, FA, FB>(exact, a, stream);
     default: return hipErrorInvalidValue;
     }
 }

@@ -32,16 +32,14 @@ hipError_t launch_linear(int cfg, bool exact, int fa, int fw, const LinArgs& a, 
     return fw == 0 ? launch_linear_fmt<1, 0>(cfg, exact, a, stream) : launch_linear_fmt<1, 1>(cfg, exact, a, stream);
 }
 
-// A gated tile with MXFP8 output needs 32 gate and 32 up columns: its block.
 LinTile lin_tile(int cfg, const LinArgs& a)
 {
-    const int few = a.gated && a.out_type >= kMxE4M3 ? 64 : 32;
+    const int few = a.skinny == kSkinnyWide ? 64 : a.skinny == kSkinnyNarrow ? 16 : 32;
     switch (cfg) {
     case kLin256x256: return {256, 256};
     case kLin256x128: return {256, 128};
     case kLin128x128: return {128, 128};
     case kLin64x64: return {64, 64};
-    case kLinRows64: return {64, few};
     case kLinRows32: return {32, few};
     default: return {16, few};
     }
@@ -173,17 +171,22 @@ int check_stride(const char* name, int64_t ld, int64_t cols)
 // -------------------------------------------------------------- product ----
 
 // The tile configuration for a product.  Few rows (of an average expert):
-// the weights' bytes are the cost, and the skinny kernel streams them.
+// the weights' bytes are the cost, and the skinny kernel streams them.  An
+// expert with more rows than the tile reads its weights again, so by expert
+// the limit is lower: 16-row tiles against 64 x 64 ones took 52 against 142
+// us at 4 rows per expert (64 tokens x 8 over 128 experts, 2048 x 768), 353
+// against 340 us at 8 (64 x 8 over 64, 4096 x 4096; 32-row tiles 325), 625
+// against 385 us at 32.  Dense, 32 x 2048 x 7168: 17.8 against 21.9 us; 64
+// rows: 31 against 24 us.
 // Otherwise the largest tile that still gives every compute unit one.
 int choose_tile(const mxg::LinArgs& a, bool exact, int cus)
 {
-    const int64_t r = a.mode == mxg::kByRows ? (a.rows + a.groups - 1) / a.groups : a.rows;
-    if (r <= 16)
+    const bool by = a.mode == mxg::kByRows;
+    const int64_t r = by ? (a.rows + a.groups - 1) / a.groups : a.rows;
+    if (r <= (by ? 6 : 16))
         return mxg::kLinRows16;
-    if (r <= 32)
+    if (r <= (by ? 16 : 32))
         return mxg::kLinRows32;
-    if (r <= 64)
-        return mxg::kLinRows64;
     const int64_t groups = a.mode == mxg::kDense ? 1 : a.groups;
     for (int cfg = exact ? mxg::kLin256x128 : mxg::kLin256x256; cfg < mxg::kLin64x64; ++cfg) {
         const mxg::LinTile t = mxg::lin_tile(cfg, a);
@@ -193,6 +196,21 @@ int choose_tile(const mxg::LinArgs& a, bool exact, int cus)
     }
     return mxg::kLin64x64;
 }
+
+// K splits of a dense product of 64 x 64 tiles: as many work-groups as
+// compute units, each with two K-steps at least for each of its four groups.
+// (64 x 2048 x 7168 exact, 32 tiles: 24 us unsplit.)
+int choose_split(const mxg::LinArgs& a, int cus)
+{
+    const int64_t tiles = (int64_t)((a.rows + 63) / 64) * ((a.N + 63) / 64);
+    int64_t s = cus / tiles;
+    const int64_t most = a.K / mxg::kGroupK / 8;
+    s = s < most ? s : most;
+    return (int)(s < 1 ? 1 : s);
+}
+
+// Sums of all splits; no more than the 64 x 64 tiles of every compute unit.
+int64_t split_bytes(const mxg::LinArgs& a, int split) { return (int64_t)split * a.rows * a.N * 4; }
 
 int check_linear(const mxgemm_linear_t* g, mxg::LinArgs* a)
 {
@@ -287,14 +305,29 @@ int check_linear(const mxgemm_linear_t* g, mxg::LinArgs* a)
 }
 
 // Tiles of configuration cfg and their order.
-int plan_linear(mxg::LinArgs* a, int cfg, int cus)
+int plan_linear(mxg::LinArgs* a, int cfg, int cus, int64_t workspace_bytes)
 {
+    a->split = 1;
+    if (cfg == mxg::kLin64x64 && a->mode == mxg::kDense) {
+        const int split = choose_split(*a, cus);
+        if (split_bytes(*a, split) <= workspace_bytes)
+            a->split = split;
+    }
+    // Skinny tiles (measurements at their launch): few tiles of a long K take
+    // many waves each; many short ones are better as small work-groups
+    a->skinny = mxg::kSkinny8;
+    if (a->gated && a->out_type >= mxg::kMxE4M3)
+        a->skinny = mxg::kSkinnyWide;
+    else if (a->mode == mxg::kDense && !a->gated && a->out_type < mxg::kMxE4M3 && (a->N + 31) / 32 < cus)
+        a->skinny = mxg::kSkinnyNarrow;
+    else if (a->mode != mxg::kDense)
+        a->skinny = a->K <= 8 * mxg::kGroupK ? mxg::kSkinny2 : mxg::kSkinny4;
     const mxg::LinTile t = mxg::lin_tile(cfg, *a);
     int64_t tiles_m = ((int64_t)a->rows + t.tile_m - 1) / t.tile_m;
     if (a->mode == mxg::kByRows)    // every expert, and the rows of none, may end inside a tile
         tiles_m = a->rows / t.tile_m + (a->groups + 1 < a->rows ? a->groups + 1 : a->rows);
     const int64_t tiles_n = ((int64_t)a->N + t.tile_n - 1) / t.tile_n;
-    const int64_t work = tiles_m * tiles_n * (a->mode == mxg::kByInner ? a->groups : 1);
+    const int64_t work = tiles_m * tiles_n * a->split * (a->mode == mxg::kByInner ? a->groups : 1);
     if (work >= (1LL << 31))
         return fail(MXGEMM_EUNSUPPORTED, "too many work items");
     a->tiles_m = (int)tiles_m;
@@ -303,9 +336,9 @@ int plan_linear(mxg::LinArgs* a, int cfg, int cus)
     // group width: about a square patch of tiles per XCD per round of
     // resident work-groups; skinny tiles share no rows of w, so theirs run
     // along N
-    const int64_t per_xcd = ((work < cus ? work : cus) + mxg::kNumXcd - 1) / mxg::kNumXcd;
+    const int64_t per_xcd = ((work < cus ? work : cus) + mxg::kNumXcd - 1) / mxg::kNumXcd / a->split;
     int64_t g = (int64_t)floor(sqrt((double)(per_xcd > 1 ? per_xcd : 1)));
-    if (cfg >= mxg::kLinRows64)
+    if (cfg >= mxg::kLinRows32)
         g = tiles_n;
     a->group_n = (int)(g < 1 ? 1 : g > tiles_n ? tiles_n : g);
     return MXGEMM_OK;
@@ -470,6 +503,14 @@ int mxgemm_combine_tokens_backward(const void* d_out, int64_t ld_d_out, const vo
     return MXGEMM_OK;
 }
 
+int64_t mxgemm_linear_workspace(int64_t rows, int64_t N, int64_t K)
+{
+    // sums of at most one 64 x 64 tile per compute unit
+    if (rows < 1 || N < 1 || K < 2048 || (rows + 63) / 64 * ((N + 63) / 64) > 128 || rows <= 32)
+        return 0;
+    return 256LL * 64 * 64 * 4;
+}
+
 int mxgemm_linear(const mxgemm_linear_t* args, void* stream)
 {
     if (!args)
@@ -494,11 +535,15 @@ int mxgemm_linear(const mxgemm_linear_t* args, void* stream)
                            {args->out, "out", size, false},
                            {mx ? args->out_scale : nullptr, "out_scale", 1, !mx},
                            {args->z, "z", 2, true},
+                           {args->workspace, "workspace", 16, true},
                            {a.groups ? args->offsets : nullptr, "offsets", 4, true}};
     TRY(check_buffers(bufs, dev));
     const int cfg = args->tile_cfg >= 0 ? args->tile_cfg : choose_tile(a, exact, cus);
-    TRY(plan_linear(&a, cfg, cus));
+    TRY(plan_linear(&a, cfg, cus, args->workspace ? args->workspace_bytes : 0));
+    a.part = (float*)args->workspace;
     HIP_TRY(mxg::launch_linear(cfg, exact, args->a_format, args->w_format, a, (hipStream_t)stream));
+    if (a.split > 1)
+        HIP_TRY(mxg::launch_linear_finish(a, (hipStream_t)stream));
     return MXGEMM_OK;
 }
 
