@@ -150,7 +150,7 @@ typedef struct mxgemm_linear {
     int32_t a_format, w_format;   /* MXGEMM_FMT_*       */
     int32_t precision;            /* MXGEMM_PRECISION_* */
     int32_t bias_type, act, gated, out_type;
-    int32_t tile_cfg;             /* -1: chosen by the sizes (tests force one, 0 .. 5) */
+    int32_t tile_cfg;             /* -1: chosen by the sizes (tests force one, 0 .. 4) */
     void* workspace;              /* 16-byte aligned, or NULL                          */
     int64_t workspace_bytes;
 } mxgemm_linear_t;

@@ -89,4 +89,25 @@ __device__ __forceinline__ float activate_grad(int act, float z, float& y)
     }
 }
 
+// z becomes act'(z), y gets act(z): one branch for all values.
+template <int N>
+__device__ __forceinline__ void activate_grads(int act, float (&z)[N], float (&y)[N])
+{
+    auto each = [&](int which) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            z[u] = activate_grad(which, z[u], y[u]);
+    };
+    if (act == kActSilu)
+        each(kActSilu);
+    else if (act == kActGeluTanh)
+        each(kActGeluTanh);
+    else if (act == kActGelu)
+        each(kActGelu);
+    else if (act == kActRelu)
+        each(kActRelu);
+    else
+        each(kActNone);
+}
+
 }  // namespace mxg

@@ -773,8 +773,9 @@ __host__ __device__ constexpr int copies_in_part(int part, int nparts)
 // Its K loop: sums the K-steps of one K group into `tot`.  src_of(s): the
 // sources of the group's K-step s.  With RAGGED only the first `valid` of the
 // nsteps steps (at least nsteps - 1 of them) are the group's own, and src_of
-// stays in range for the others.  On return this wave's copies have landed.
-template <int BM, int BN, int WGM, int WGN, int WGK, int FA, int FB, bool RAGGED, class Src>
+// stays in range for the others.  EARLY: the copies of step 1 do not wait for
+// step 0 (work items of few K-steps).  On return this wave's copies have landed.
+template <int BM, int BN, int WGM, int WGN, int WGK, int FA, int FB, bool RAGGED, bool EARLY, class Src>
 __device__ __forceinline__ void exact_mainloop(uint8_t* stage0, uint8_t* stage1,
                                                const CopyOffsets<BM, BN, WGM * WGN, 32>& co, const Src& src_of,
                                                int nsteps, int valid, int wk, int wl, int lane,
@@ -830,10 +831,22 @@ __device__ __forceinline__ void exact_mainloop(uint8_t* stage0, uint8_t* stage1,
     uint32_t sw[NF];           // scale words (4 MX blocks) of a K-step
 
     copy_issue(co, src_of(0), stage0 + ksub, wl);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (nsteps > 1)
-        copy_issue(co, src_of(1), stage1 + ksub, wl);
+    if constexpr (EARLY) {
+        // both first steps on their way: step 0 has landed once at most
+        // the copies that every wave issues for step 1 are outstanding
+        if (nsteps > 1) {
+            copy_issue(co, src_of(1), stage1 + ksub, wl);
+            wait_copies<G::IA / NWG + G::IB / NWG>();
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        __syncthreads();
+    } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (nsteps > 1)
+            copy_issue(co, src_of(1), stage1 + ksub, wl);
+    }
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
         sw[f] = *reinterpret_cast<const uint32_t*>(stage0 + scale_off(f));
@@ -999,7 +1012,7 @@ mxgemm_exact_kernel(GemmArgs p)
         auto src_of = [&](int s) { return step_src(p, seg0, n0, WGK * s + wk); };
 
         v16f tot[GA][GB];          // running totals of the finished pairs
-        exact_mainloop<BM, BN, WGM, WGN, WGK, FA, FB, false>(stage0, stage1, co, src_of, nsteps, nsteps, wk, wl,
+        exact_mainloop<BM, BN, WGM, WGN, WGK, FA, FB, false, false>(stage0, stage1, co, src_of, nsteps, nsteps, wk, wl,
                                                              lane, tot);
 
         if constexpr (WGK > 1) {

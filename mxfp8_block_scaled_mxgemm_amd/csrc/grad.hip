@@ -35,114 +35,210 @@ __device__ __forceinline__ void load8(int type, const void* base, int64_t at, in
         load8<kFP32>(base, at, c, n, v);
 }
 
-// A work-group takes 128 tokens x 64 columns of dz.  Thread (rl, cl) computes
-// eight columns of rows rl, rl + 32, ...: dz = d_out act'(z), or, gated, the
-// column's half of [d_out u act'(g), d_out act(g)].  Along the columns, four
-// threads share a block of 32 and quantise it at once.  The FP32 values also
-// go to LDS, transposed to [column][token] and padded so that neither side
-// piles onto a few banks; there a thread takes one column's block of 32
-// tokens: its sum, its scale, its codes (32 bytes; four threads write one
-// column's 128 bytes).  Tokens past the expert's last one count as zeros, so
-// blocks never cross experts.  Bound by memory: d_out and z are read once
-// and the two bytes per element written.
+// Eight 16-bit elements as loaded.
+struct Raw16 {
+    u32x4 v;
+    __device__ __forceinline__ void load(const void* base, int64_t at)
+    {
+        v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at);
+    }
+    __device__ __forceinline__ void get(int type, float (&f)[8]) const
+    {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t w = v[u >> 1];
+            f[u] = type == kFP16 ? Element<kFP16>::get((uint16_t)(w >> (16 * (u & 1))))
+                                 : __uint_as_float(u & 1 ? w & 0xFFFF0000u : w << 16);
+        }
+    }
+};
+
+// A work-group takes 128 tokens x 64 columns of dz; gated with halves of whole
+// blocks (FUSED), 32 columns of both halves, [d_out u act'(g), d_out act(g)],
+// so that d_out and z are read and the activation is evaluated once.  A
+// thread computes eight columns (FUSED: eight of each half) of a few rows;
+// the loads of all its rows go out before the first is used.  Along the
+// columns, four threads share a block of 32 and quantise it at once.  The
+// FP32 values also go to LDS, transposed to [column][token] and padded so
+// that neither side piles onto a few banks; there a thread takes one column's
+// block of 32 tokens: its sum, its scale, its codes (32 bytes; four threads
+// write one column's 128 bytes).  Tokens past the expert's last one count as
+// zeros, so blocks never cross experts.  Bound by memory: d_out and z are
+// read once and the two bytes per element written.
 constexpr int kGradRows = 128, kGradCols = 64, kGradLd = kGradRows + 1;
 
+// First token of a chunk of 128 and the end of its expert; false past the
+// last segment.
+__device__ __forceinline__ bool grad_rows(const GradArgs& p, int chunk, int& row0, int& end)
+{
+    row0 = chunk * kGradRows;
+    end = p.rows;
+    if (!p.offsets)
+        return true;
+    // the expert whose padded segment holds this chunk
+    const int at = row0;
+    if (at >= p.k_offsets[p.groups])
+        return false;
+    int lo = 0, hi = p.groups;              // k_offsets[lo] <= at < k_offsets[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (p.k_offsets[mid] <= at)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    row0 = p.offsets[lo] + at - p.k_offsets[lo];
+    end = p.offsets[lo + 1];
+    end = end < p.rows ? end : p.rows;
+    row0 = row0 < 0 ? 0 : row0;
+    return true;
+}
+
+// dz of columns [c, c + 8) of one row, the general way: any width and gating.
+__device__ __forceinline__ void grad_columns(const GradArgs& p, int64_t row, int c, float (&dz)[8])
+{
+    const int half = p.N / 2;
+    // the thread's columns as [first, first + 8) of d_out: a gated piece that
+    // reaches over the middle is taken a column at a time
+    const bool up = p.gated && c >= half;
+    if (!p.gated || up || c + 8 <= half) {
+        const int width = p.gated ? half : p.N;
+        const int first = up ? c - half : c;
+        load8(p.d_type, p.d, row * p.ld_d, first, width, dz);
+        if (p.z && (p.gated || p.act != kActNone)) {
+            float z[8], z1[8], y[8];
+            load8<kBF16>(p.z, row * p.ld_z, first, width, z);
+            if (p.gated)
+                load8<kBF16>(p.z, row * p.ld_z + half, first, width, z1);
+            activate_grads(p.act, z, y);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                dz[u] *= p.gated ? (up ? y[u] : z[u] * z1[u]) : z[u];
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int u = 0; u < 8 && c + u < p.N; ++u) {
+        const bool hi = c + u >= half;
+        const int col = hi ? c + u - half : c + u;
+        float d1[8], z[8], z1[8], y[8];
+        load8(p.d_type, p.d, row * p.ld_d, col, col + 1, d1);
+        load8<kBF16>(p.z, row * p.ld_z, col, col + 1, z);
+        load8<kBF16>(p.z, row * p.ld_z + half, col, col + 1, z1);
+        activate_grads(p.act, z, y);
+        const float x = d1[0] * (hi ? y[0] : z[0] * z1[0]);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            dz[v] = v == u ? x : dz[v];
+    }
+}
+
+// Eight columns of dz along the columns, and to LDS (tile column tc, row r).
 template <int F>
+__device__ __forceinline__ void grad_put(const GradArgs& p, float* t, int row, int r, int end, int c, int tc,
+                                         const float (&dz)[8], int lane)
+{
+    if (p.q) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            m = max(m, __float_as_uint(dz[u]) & 0x7FFFFFFFu);
+        const MxScale s = mx_scale<F>(quad_max(m));
+        if (row < end && c < p.ld_q) {
+            *reinterpret_cast<u32x2*>(p.q + row * p.ld_q + c) =
+                u32x2{mx_codes<F>(s, dz[0], dz[1], dz[2], dz[3]), mx_codes<F>(s, dz[4], dz[5], dz[6], dz[7])};
+            if ((lane & 3) == 0)
+                p.s[row * (p.ld_q >> 5) + (c >> 5)] = s.byte;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        t[(tc + u) * kGradLd + r] = dz[u];
+}
+
+// VEC: whole eights of 16-bit d_out (and z) columns, so a row's loads are
+// plain; rows past the end read the last one and count as zeros.
+template <int F, bool FUSED, bool VEC>
 __global__ void __launch_bounds__(256) grad_kernel(GradArgs p)
 {
     __shared__ float t[kGradCols * kGradLd];
     const int tid = threadIdx.x, lane = tid & 63;
     const int chunk = blockIdx.y;
-    const int n0 = blockIdx.x * kGradCols;
-    int row0 = chunk * kGradRows, end = p.rows;
-    if (p.offsets) {
-        // the expert whose padded segment holds this chunk
-        const int at = chunk * kGradRows;
-        if (at >= p.k_offsets[p.groups])
-            return;
-        int lo = 0, hi = p.groups;              // k_offsets[lo] <= at < k_offsets[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (p.k_offsets[mid] <= at)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        row0 = p.offsets[lo] + at - p.k_offsets[lo];
-        end = p.offsets[lo + 1];
-        end = end < p.rows ? end : p.rows;
-        row0 = row0 < 0 ? 0 : row0;
-    }
+    int row0, end;
+    if (!grad_rows(p, chunk, row0, end))
+        return;
     const int half = p.N / 2;
-    const int cl = tid & 7, rl = tid >> 3;
-    const int c = n0 + 8 * cl;                  // first of the thread's columns
-#pragma unroll 1
-    for (int r = rl; r < kGradRows; r += 32) {
-        const int row = row0 + r;
-        float dz[8];
+    const int n0 = blockIdx.x * kGradCols;      // FUSED: columns n0 / 2 of both halves
+    constexpr int kLanes = FUSED ? 4 : 8;       // threads across the columns
+    constexpr int kPasses = kGradRows * kLanes / 256;
+    const int cl = tid % kLanes, rl = tid / kLanes;
+    const int c = (FUSED ? n0 / 2 : n0) + 8 * cl;
+    if constexpr (VEC) {
+        const int width = FUSED ? half : p.N;
+        const int cc = c < width ? c : width - 8;
+        const bool act = p.z && p.act != kActNone;
+        Raw16 d[kPasses], z[kPasses], z1[FUSED ? kPasses : 1];
+        // (rows of an empty tail read row 0 at worst: there is one)
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            dz[u] = 0.f;
-        if (row < end) {
-            // the thread's columns as [first, first + 8) of d_out: a gated
-            // piece that reaches over the middle is taken a column at a time
-            const bool up = p.gated && c >= half;
-            if (!p.gated || up || c + 8 <= half) {
-                float y;
-                const int width = p.gated ? half : p.N;
-                const int first = up ? c - half : c;
-                load8(p.d_type, p.d, row * p.ld_d, first, width, dz);
-                if (p.z && (p.gated || p.act != kActNone)) {
-                    float z[8], z1[8];
-                    load8<kBF16>(p.z, row * p.ld_z, first, width, z);
-                    if (p.gated)
-                        load8<kBF16>(p.z, row * p.ld_z + half, first, width, z1);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float slope = activate_grad(p.act, z[u], y);
-                        dz[u] *= p.gated ? (up ? y : slope * z1[u]) : slope;
-                    }
-                }
-            } else {
-#pragma unroll 1
-                for (int u = 0; u < 8 && c + u < p.N; ++u) {
-                    const bool hi = c + u >= half;
-                    const int col = hi ? c + u - half : c + u;
-                    float d1[8], z[8], z1[8], y;
-                    load8(p.d_type, p.d, row * p.ld_d, col, col + 1, d1);
-                    load8<kBF16>(p.z, row * p.ld_z, col, col + 1, z);
-                    load8<kBF16>(p.z, row * p.ld_z + half, col, col + 1, z1);
-                    const float slope = activate_grad(p.act, z[0], y);
-                    const float x = d1[0] * (hi ? y : slope * z1[0]);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        dz[v] = v == u ? x : dz[v];
-                }
-            }
+        for (int k = 0; k < kPasses; ++k) {
+            int64_t row = row0 + rl + k * (256 / kLanes);
+            row = row < end ? row : end > 0 ? end - 1 : 0;
+            d[k].load(p.d, row * p.ld_d + cc);
+            if (FUSED || act)
+                z[k].load(p.z, row * p.ld_z + cc);
+            if constexpr (FUSED)
+                z1[k].load(p.z, row * p.ld_z + half + cc);
         }
-        if (p.q) {
-            uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            const int r = rl + k * (256 / kLanes), row = row0 + r;
+            const bool ok = row < end && c < width;
+            float x[8], x1[8], slope[8], y[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                m = max(m, __float_as_uint(dz[u]) & 0x7FFFFFFFu);
-            m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-            const MxScale s = mx_scale<F>(m);
-            if (row < end && c < p.ld_q) {
-                *reinterpret_cast<u32x2*>(p.q + row * p.ld_q + c) =
-                    u32x2{mx_codes<F>(s, dz[0], dz[1], dz[2], dz[3]), mx_codes<F>(s, dz[4], dz[5], dz[6], dz[7])};
-                if ((lane & 3) == 0)
-                    p.s[row * (p.ld_q >> 5) + (c >> 5)] = s.byte;
+                x[u] = 0.f;
+            if (ok)
+                d[k].get(p.d_type, x);
+            if (FUSED || act) {
+                z[k].get(kBF16, slope);
+                activate_grads(p.act, slope, y);
             }
-        }
+            if constexpr (FUSED) {
+                z1[k].get(kBF16, x1);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            t[(8 * cl + u) * kGradLd + r] = dz[u];
+                for (int u = 0; u < 8; ++u) {
+                    const float dg = x[u] * slope[u] * x1[u];
+                    x1[u] = ok ? x[u] * y[u] : 0.f;
+                    x[u] = ok ? dg : 0.f;
+                }
+            } else if (act) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    x[u] = ok ? x[u] * slope[u] : 0.f;
+            }
+            grad_put<F>(p, t, row, r, end, c, 8 * cl, x, lane);
+            if constexpr (FUSED)
+                grad_put<F>(p, t, row, r, end, half + c, 32 + 8 * cl, x1, lane);
+        }
+    } else {
+#pragma unroll 1
+        for (int r = rl; r < kGradRows; r += 256 / kLanes) {
+            const int row = row0 + r;
+            float dz[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                dz[u] = 0.f;
+            if (row < end)
+                grad_columns(p, row, c, dz);
+            grad_put<F>(p, t, row, r, end, c, 8 * cl, dz, lane);
+        }
     }
     if (!p.qt && !p.part)
         return;
     __syncthreads();
     const int col = tid >> 2, b = tid & 3;      // column, block of 32 tokens
+    const int n = FUSED ? n0 / 2 + (col & 31) + (col >= 32 ? half : 0) : n0 + col;
+    const bool there = FUSED ? n0 / 2 + (col & 31) < half : n < p.N;
     const float* v = t + col * kGradLd + 32 * b;
     float x[32], sum = 0.f;
     uint32_t m = 0;
@@ -155,20 +251,35 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs p)
     if (p.part) {
         sum += __shfl_xor(sum, 1);
         sum += __shfl_xor(sum, 2);
-        if (b == 0 && n0 + col < p.N)
-            p.part[(int64_t)chunk * p.N + n0 + col] = sum;
+        if (b == 0 && there)
+            p.part[(int64_t)chunk * p.N + n] = sum;
     }
-    if (p.qt && n0 + col < p.N) {
+    if (p.qt && there) {
         const MxScale s = mx_scale<F>(m);
         u32x4 code[2];
 #pragma unroll
         for (int w = 0; w < 8; ++w)
             code[w >> 2][w & 3] = mx_codes<F>(s, x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3]);
-        const int64_t at = (n0 + col) * p.ld_qt + (int64_t)chunk * kGradRows + 32 * b;
+        const int64_t at = n * p.ld_qt + (int64_t)chunk * kGradRows + 32 * b;
         *reinterpret_cast<u32x4*>(p.qt + at) = code[0];
         *reinterpret_cast<u32x4*>(p.qt + at + 16) = code[1];
         p.st[at >> 5] = s.byte;
     }
+}
+
+// Zero codes of the row codes' padding, columns [N, ld_q) (whole blocks past
+// the last column's; FUSED tiles do not reach them).
+__global__ void __launch_bounds__(256) grad_pad_kernel(GradArgs p)
+{
+    const int first = (p.N + 31) / 32 * 32, width = (int)p.ld_q - first;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / width;
+    const int c = first + (int)(i % width);
+    if (row >= p.rows)
+        return;
+    p.q[row * p.ld_q + c] = 0;
+    if (c % 32 == 0)
+        p.s[row * (p.ld_q >> 5) + c / 32] = 0;
 }
 
 // d_bias[e][n]: the column sums of the expert's tiles, in order.
@@ -192,16 +303,37 @@ __global__ void __launch_bounds__(256) grad_bias_kernel(GradArgs p)
     p.d_bias[(int64_t)e * p.N + n] = sum;
 }
 
+template <int F>
+static void grad_launch(const GradArgs& a, hipStream_t stream)
+{
+    auto aligned = [](const void* p, int64_t ld) { return (ld & 7) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    const int width = a.gated ? a.N / 2 : a.N;
+    const bool vec = a.rows > 0 && a.d_type != kFP32 && (width & 7) == 0 && aligned(a.d, a.ld_d) &&
+                     (!a.z || aligned(a.z, a.ld_z));
+    if (vec && a.gated && (width & 31) == 0) {
+        const dim3 grid((unsigned)(width / 32), (unsigned)a.chunks);
+        hipLaunchKernelGGL((grad_kernel<F, true, true>), grid, dim3(256), 0, stream, a);
+        if (a.q && a.ld_q > a.N)
+            hipLaunchKernelGGL(grad_pad_kernel, dim3((unsigned)((a.rows * (a.ld_q - a.N) + 255) / 256)), dim3(256), 0,
+                               stream, a);
+        return;
+    }
+    // columns up to the row codes' padded width (their padding is written too)
+    const int64_t all = a.q ? a.ld_q : a.N;
+    const dim3 grid((unsigned)((all + kGradCols - 1) / kGradCols), (unsigned)a.chunks);
+    if (vec && !a.gated)
+        hipLaunchKernelGGL((grad_kernel<F, false, true>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((grad_kernel<F, false, false>), grid, dim3(256), 0, stream, a);
+}
+
 hipError_t launch_grad(const GradArgs& a, hipStream_t stream)
 {
-    // columns up to the row codes' padded width (their padding is written too)
-    const int64_t width = a.q ? a.ld_q : a.N;
-    const dim3 grid((unsigned)((width + kGradCols - 1) / kGradCols), (unsigned)a.chunks);
     if (a.chunks > 0) {
         if (a.fmt == kE5M2)
-            hipLaunchKernelGGL(grad_kernel<kE5M2>, grid, dim3(256), 0, stream, a);
+            grad_launch<kE5M2>(a, stream);
         else
-            hipLaunchKernelGGL(grad_kernel<kE4M3>, grid, dim3(256), 0, stream, a);
+            grad_launch<kE4M3>(a, stream);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.d_bias)

@@ -7,14 +7,18 @@ namespace mxg {
 
 // dst[b][c][r] = src[b][r][c].  A work-group takes 128 x 128 bytes; a thread
 // takes 4 rows x 16 columns, turned in registers into one word of four row
-// bytes per column, so LDS and the stores move words and 16-byte pieces.
-// Rows of LDS are 36 words apart: 16-byte aligned, spread over the banks.
+// bytes per column, so LDS and the stores move words and 16-byte pieces.  In
+// LDS a column's eight 16-byte pieces are XOR-swizzled by bits 4-6 of the
+// column: the eight threads that write columns 16 apart meet different banks.
 // Bound by memory: every byte read and written once.
-constexpr int kTurn = 128, kTurnLd = 36;
+constexpr int kTurn = 128;
+
+// Word w of column c.
+__device__ __forceinline__ int turn_at(int c, int w) { return c * (kTurn / 4) + (w ^ (4 * (c >> 4))); }
 
 __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p)
 {
-    __shared__ __attribute__((aligned(16))) uint32_t t[kTurn * kTurnLd];
+    __shared__ __attribute__((aligned(16))) uint32_t t[kTurn * kTurn / 4];
     const int tid = threadIdx.x;
     const int64_t r0 = (int64_t)blockIdx.y * kTurn, c0 = (int64_t)blockIdx.x * kTurn;
     const uint8_t* src = p.src + blockIdx.z * p.src_batch;
@@ -23,23 +27,19 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p)
         const int cl = (tid & 7) * 16, rl = (tid >> 3) * 4;
         const int64_t c = c0 + cl;
         uint32_t in[4][4];
+        const uint8_t* row = src + (r0 + rl) * p.ld_src + c;
+        if (r0 + kTurn <= p.rows && c0 + kTurn <= p.cols) {     // no lane branches: the loads go out together
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + rl + i;
+            for (int i = 0; i < 4; ++i)
+                __builtin_memcpy(in[i], row + i * p.ld_src, 16);
+        } else {
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-                in[i][w] = 0;
-            if (r >= p.rows)
-                continue;
-            const uint8_t* row = src + r * p.ld_src + c;
-            if (c + 16 <= p.cols) {
-                __builtin_memcpy(in[i], row, 16);
-            } else {
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    if (c + u < p.cols)
-                        in[i][u >> 2] |= (uint32_t)row[u] << (8 * (u & 3));
-            }
+                for (int u = 0; u < 16; ++u) {
+                    const uint32_t x = r0 + rl + i < p.rows && c + u < p.cols ? row[i * p.ld_src + u] : 0;
+                    in[i][u >> 2] = (u & 3 ? in[i][u >> 2] : 0) | x << (8 * (u & 3));
+                }
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -48,11 +48,11 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p)
             const uint32_t hi01 = __builtin_amdgcn_perm(in[1][w], in[0][w], 0x07030602u);
             const uint32_t lo23 = __builtin_amdgcn_perm(in[3][w], in[2][w], 0x05010400u);
             const uint32_t hi23 = __builtin_amdgcn_perm(in[3][w], in[2][w], 0x07030602u);
-            uint32_t* o = t + (cl + 4 * w) * kTurnLd + (rl >> 2);
-            o[0 * kTurnLd] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
-            o[1 * kTurnLd] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
-            o[2 * kTurnLd] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
-            o[3 * kTurnLd] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+            const int o = turn_at(cl, rl >> 2) + 4 * w * (kTurn / 4);       // cl: multiples of 16
+            t[o] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+            t[o + kTurn / 4] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+            t[o + 2 * (kTurn / 4)] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+            t[o + 3 * (kTurn / 4)] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
         }
     }
     __syncthreads();
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p)
         const int64_t c = c0 + cl, r = r0 + rl;
         if (c >= p.cols || r >= p.rows)
             continue;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(t + cl * kTurnLd + (rl >> 2));
+        const u32x4 v = *reinterpret_cast<const u32x4*>(t + turn_at(cl, rl >> 2));
         uint8_t* out = dst + c * p.rows + r;
         if (r + 16 <= p.rows) {
             __builtin_memcpy(out, &v, 16);

@@ -52,12 +52,11 @@ struct LinArgs {
 // Tile configurations of the product
 enum {
     kLin256x256 = 0,              // native only: four waves of 128 x 128
-    kLin256x128 = 1,
-    kLin128x128 = 2,
-    kLin64x64 = 3,                // four K groups
-    kLinRows32 = 4,               // 32 or 16 rows, weights straight to registers
-    kLinRows16 = 5,
-    kLinCfgs = 6
+    kLin128x128 = 1,              // four waves of 64 x 64, two work-groups per compute unit
+    kLin64x64 = 2,                // four K groups
+    kLinRows32 = 3,               // 32 or 16 rows, weights straight to registers
+    kLinRows16 = 4,
+    kLinCfgs = 5
 };
 
 // Skinny tiles: 16 columns and sixteen waves; 32 columns and 2, 4 or 8 waves;

@@ -27,19 +27,26 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(LinArgs p)
             z1[u] = 0.f;
     }
     const float* src = p.part + (int64_t)row * p.N;
-    for (int k = 0; k < p.split; ++k, src += (int64_t)p.rows * p.N)
+    const int64_t plane = (int64_t)p.rows * p.N;
+    for (int k0 = 0; k0 < p.split; k0 += 8) {
+        // eight splits' loads at a time; those past the last read it again
+        Raw8 x[8][GATED ? 2 : 1];
 #pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            const Raw8 x = raw8(kFP32, src, h * cols, c, cols);
+        for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float v = __uint_as_float(x.v[u >> 2][u & 3]);
-                if constexpr (GATED)
-                    (h ? z1 : z)[u] += v;
-                else
-                    z[u] += v;
+            for (int h = 0; h < (GATED ? 2 : 1); ++h)
+                x[k][h] = raw8(kFP32, src + (k0 + k < p.split ? k0 + k : p.split - 1) * plane, h * cols, c, cols);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < p.split) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    z[u] += __uint_as_float(x[k][0].v[u >> 2][u & 3]);
+                    if constexpr (GATED)
+                        z1[u] += __uint_as_float(x[k][1].v[u >> 2][u & 3]);
+                }
             }
-        }
+    }
     finish<GATED, 1, 1>(p, 0, row, c, cols, ok ? 1 : 0, z, z1, bias, res, threadIdx.x & 63);
 }
 

@@ -887,9 +887,10 @@ __device__ __forceinline__ void groups_partial(const LinArgs& p, uint8_t* lds, v
 // free: the accumulators go through LDS in slabs of 32 rows x 64 columns, so
 // that bias, activation, residual and the stores run on whole rows; the K
 // groups' slabs are added there in group order.
-template <int BM, int BN, int WGM, int WGN, int WGK, bool EXACT, int FA, int FB>
+// WGS work-groups share a compute unit.
+template <int BM, int BN, int WGM, int WGN, int WGK, int WGS, bool EXACT, int FA, int FB>
 __global__ void __launch_bounds__(WGM * WGN * WGK * 64)
-    __attribute__((amdgpu_waves_per_eu(WGM * WGN * WGK / 4, WGM * WGN * WGK / 4)))
+    __attribute__((amdgpu_waves_per_eu(WGM * WGN * WGK * WGS / 4, WGM * WGN * WGK * WGS / 4)))
 linear_kernel(LinArgs p)
 {
     constexpr int NWG = WGM * WGN;
@@ -901,7 +902,7 @@ linear_kernel(LinArgs p)
     constexpr int kWaveEpilogue = kSlabBytes + TM * TN * 2;      // a slab and a 16-bit residual
     constexpr int kLoop = WGK * (EXACT ? 2 * G::STAGE : R::BYTES);
     constexpr int kLds = WGK == 1 && NWG * kWaveEpilogue > kLoop ? NWG * kWaveEpilogue : kLoop;
-    static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+    static_assert(WGS * kLds <= 160 * 1024, "LDS of a compute unit");
 
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
@@ -947,7 +948,7 @@ linear_kernel(LinArgs p)
                 return StepSrc{uniform(src0.a + (int64_t)k * kBK), uniform(src0.b + (int64_t)k * kBK),
                                uniform(src0.as + k * 4), uniform(src0.bs + k * 4)};
             };
-            exact_mainloop<BM, BN, WGM, WGN, WGK, FA, FB, (WGK > 1)>(lds, lds + WGK * G::STAGE, co, src_of, nsteps,
+            exact_mainloop<BM, BN, WGM, WGN, WGK, FA, FB, (WGK > 1), true>(lds, lds + WGK * G::STAGE, co, src_of, nsteps,
                                                                      valid, wk, wl, lane, acc);
         } else {
             PairCopies<BM, BN, NWG> co;
@@ -1199,19 +1200,19 @@ __global__ void __launch_bounds__(NW * 64) linear_skinny_kernel(LinArgs p)
 
 // ------------------------------------------------------------------ launch --
 
-template <int BM, int BN, int WGM, int WGN, int EWM, int EWN, int WGK, int FA, int FB>
+template <int BM, int BN, int WGM, int WGN, int WGK, int WGS, int FA, int FB>
 static hipError_t launch_lin_tile(bool exact, const LinArgs& a, hipStream_t stream)
 {
     if (exact) {
-        if constexpr ((BM / EWM) * (BN / EWN) <= 64 * 64) {
-            hipLaunchKernelGGL((linear_kernel<BM, BN, EWM, EWN, WGK, true, FA, FB>), dim3(a.total_work),
-                               dim3(EWM * EWN * WGK * 64), 0, stream, a);
+        if constexpr ((BM / WGM) * (BN / WGN) <= 64 * 64) {
+            hipLaunchKernelGGL((linear_kernel<BM, BN, WGM, WGN, WGK, WGS, true, FA, FB>), dim3(a.total_work),
+                               dim3(WGM * WGN * WGK * 64), 0, stream, a);
             return hipGetLastError();
         } else {
             return hipErrorInvalidValue;    // never planned
         }
     }
-    hipLaunchKernelGGL((linear_kernel<BM, BN, WGM, WGN, WGK, false, FA, FB>), dim3(a.total_work),
+    hipLaunchKernelGGL((linear_kernel<BM, BN, WGM, WGN, WGK, WGS, false, FA, FB>), dim3(a.total_work),
                        dim3(WGM * WGN * WGK * 64), 0, stream, a);
     return hipGetLastError();
 }
@@ -1249,10 +1250,9 @@ template <int FA, int FB>
 hipError_t launch_linear_fmt(int cfg, bool exact, const LinArgs& a, hipStream_t stream)
 {
     switch (cfg) {
-    case kLin256x256: return launch_lin_tile<256, 256, 2, 2, 2, 2, 1, FA, FB>(exact, a, stream);
-    case kLin256x128: return launch_lin_tile<256, 128, 2, 2, 4, 2, 1, FA, FB>(exact, a, stream);
-    case kLin128x128: return launch_lin_tile<128, 128, 2, 2, 2, 2, 1, FA, FB>(exact, a, stream);
-    case kLin64x64: return launch_lin_tile<64, 64, 1, 1, 1, 1, 4, FA, FB>(exact, a, stream);
+    case kLin256x256: return launch_lin_tile<256, 256, 2, 2, 1, 1, FA, FB>(exact, a, stream);
+    case kLin128x128: return launch_lin_tile<128, 128, 2, 2, 1, 2, FA, FB>(exact, a, stream);
+    case kLin64x64: return launch_lin_tile<64, 64, 1, 1, 4, 1, FA, FB>(exact, a, stream);
     case kLinRows32: return launch_lin_rows<2, FA, FB>(exact, a, stream);
     case kLinRows16: return launch_lin_rows<1, FA, FB>(exact, a, stream);
     default: return hipErrorInvalidValue;

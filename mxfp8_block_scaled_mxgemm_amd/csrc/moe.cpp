@@ -37,7 +37,6 @@ LinTile lin_tile(int cfg, const LinArgs& a)
     const int few = a.skinny == kSkinnyWide ? 64 : a.skinny == kSkinnyNarrow ? 16 : 32;
     switch (cfg) {
     case kLin256x256: return {256, 256};
-    case kLin256x128: return {256, 128};
     case kLin128x128: return {128, 128};
     case kLin64x64: return {64, 64};
     case kLinRows32: return {32, few};
@@ -171,30 +170,32 @@ int check_stride(const char* name, int64_t ld, int64_t cols)
 // -------------------------------------------------------------- product ----
 
 // The tile configuration for a product.  Few rows (of an average expert):
-// the weights' bytes are the cost, and the skinny kernel streams them.  An
-// expert with more rows than the tile reads its weights again, so by expert
-// the limit is lower: 16-row tiles against 64 x 64 ones took 52 against 142
-// us at 4 rows per expert (64 tokens x 8 over 128 experts, 2048 x 768), 353
-// against 340 us at 8 (64 x 8 over 64, 4096 x 4096; 32-row tiles 325), 625
-// against 385 us at 32.  Dense, 32 x 2048 x 7168: 17.8 against 21.9 us; 64
-// rows: 31 against 24 us.
-// Otherwise the largest tile that still gives every compute unit one.
+// the weights' bytes are the cost, and the skinny kernel streams them (4 rows
+// per expert, 64 tokens x 8 over 128 experts, 2048 x 768: 52 us).  An expert
+// with more rows than the tile reads its weights again, so from 8 rows per
+// expert on the 128 x 128 tiles stream them better (native, 64 x 8 over 64,
+// 4096 x 4096: 250 us against 351; exact, 299 against 356).  Dense, 32 x 2048
+// x 7168: 17.8 against 21.9 us with 64 x 64 tiles; 64 rows: 31 against 24 us.
+// Otherwise 128 x 128 tiles, two of whose work-groups share a compute unit (the
+// epilogue of one runs beside the K loop of the other), where they occupy more
+// than half of the compute units (1024 x 2048 x 4096, 128 tiles: 35 against 31
+// us with 64 x 64 ones, exact).  Native dense products of a long K take 256 x
+// 256 tiles, which ask the L2 for half the bytes: 8192 x 8192 x 8192, 485
+// against 584 us; x 2048, 163 against 169; x 512, 88 against 71.
 int choose_tile(const mxg::LinArgs& a, bool exact, int cus)
 {
     const bool by = a.mode == mxg::kByRows;
     const int64_t r = by ? (a.rows + a.groups - 1) / a.groups : a.rows;
     if (r <= (by ? 6 : 16))
         return mxg::kLinRows16;
-    if (r <= (by ? 16 : 32))
+    if (r <= 32 && !by)
         return mxg::kLinRows32;
-    const int64_t groups = a.mode == mxg::kDense ? 1 : a.groups;
-    for (int cfg = exact ? mxg::kLin256x128 : mxg::kLin256x256; cfg < mxg::kLin64x64; ++cfg) {
-        const mxg::LinTile t = mxg::lin_tile(cfg, a);
-        const int64_t tiles = groups * ((r + t.tile_m - 1) / t.tile_m) * ((a.N + t.tile_n - 1) / t.tile_n);
-        if (tiles >= cus)
-            return cfg;
-    }
-    return mxg::kLin64x64;
+    auto tiles = [&](int64_t m, int64_t n) {
+        return (a.mode == mxg::kDense ? 1 : a.groups) * ((r + m - 1) / m) * ((a.N + n - 1) / n);
+    };
+    if (!exact && a.mode == mxg::kDense && tiles(256, 256) >= cus && a.K >= 2048)
+        return mxg::kLin256x256;
+    return tiles(128, 128) > cus / 2 ? mxg::kLin128x128 : mxg::kLin64x64;
 }
 
 // K splits of a dense product of 64 x 64 tiles: as many work-groups as

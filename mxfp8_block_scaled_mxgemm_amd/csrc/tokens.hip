@@ -76,21 +76,39 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs p)
             tot[e] = run;
             before[e] = 0;
         }
-        if (MODE == kSortPlace) {
-            uint32_t all = 0, pre = 0;
-#pragma unroll 8
-            for (int b = 0; b < p.blocks; ++b) {
-                const uint32_t t = p.ws[(int64_t)b * E1 + e];
-                pre += b < (int)blockIdx.x ? t : 0;
-                all += t;
-            }
-            tot[e] = all;
-            before[e] = pre;
-        }
+        if (MODE == kSortPlace)
+            tot[e] = before[e] = 0;
     }
     if (MODE == kSortCount)
         return;
     __syncthreads();
+    if (MODE == kSortPlace) {
+        // Sums over the work-groups of every key, and over those before this
+        // one: the threads left over by the keys share the work-groups (sums
+        // of counts: their order does not matter).
+        const int parts = kSortThreads / E1 > 1 ? kSortThreads / E1 : 1;
+        const int share = (p.blocks + parts - 1) / parts;
+        for (int i = tid; i < parts * E1; i += kSortThreads) {
+            const int e = i % E1;
+            const int lo = i / E1 * share, hi = lo + share < p.blocks ? lo + share : p.blocks;
+            uint32_t all = 0, pre = 0;
+            for (int b0 = lo; b0 < hi; b0 += 16) {
+                uint32_t n[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u)        // all in flight; past the end, the last again
+                    n[u] = p.ws[(int64_t)(b0 + u < hi ? b0 + u : hi - 1) * E1 + e];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    n[u] = b0 + u < hi ? n[u] : 0;
+                    pre += b0 + u < (int)blockIdx.x ? n[u] : 0;
+                    all += n[u];
+                }
+            }
+            atomicAdd(&tot[e], all);
+            atomicAdd(&before[e], pre);
+        }
+        __syncthreads();
+    }
     if (wave == 0) {
         // exclusive sums over the experts, a run of them per lane
         const int per = (E1 + 63) / 64, lo = lane * per, hi = lo + per < E1 ? lo + per : E1;

@@ -10,8 +10,7 @@ from gpu_common import say, torch_cuda
 pytestmark = pytest.mark.gpu
 ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
 # tile configuration -> rows and columns of a tile, exact mode has it
-TILES = {0: (256, 256, False), 1: (256, 128, True), 2: (128, 128, True), 3: (64, 64, True), 4: (32, 32, True),
-         5: (16, 32, True)}
+TILES = {0: (256, 256, False), 1: (128, 128, True), 2: (64, 64, True), 3: (32, 32, True), 4: (16, 32, True)}
 
 
 def _operands(g, M, N, K, a_fmt="e4m3", w_fmt="e4m3", lead=()):
