@@ -31,17 +31,17 @@ struct LinItem {
     bool zero;
 };
 
-// Row tile tm of the list of all experts' row tiles: expert e has
-// ceil(rows of e / BM) of them, and the rows past the last expert come as one
-// expert more.  All 64 lanes of the wave take part, four experts each, so up
-// to 255 experts take one round of loads; the offsets are clamped to the rows
-// there are.  False past the end of the list.
+// The list of all experts' row tiles: expert e has ceil(rows of e / BM) of
+// them, and the rows past the last expert come as one expert more.  A round
+// takes 256 experts, four per lane (so up to 255 experts are one round of
+// loads); the offsets are clamped to the rows there are.  All 64 lanes of the
+// wave take part.
 template <int BM>
-__device__ __forceinline__ bool find_rows(const LinArgs& p, int tm, int lane, LinItem& it)
-{
-    int before = 0;
-    for (int g0 = 0; g0 <= p.groups; g0 += 256) {
-        int at[5], n[4], sum = 0;
+struct RowTiles {
+    int at[5], n[4], sum, inc;      // the lane's row ranges and tiles; tiles of the round up to it
+
+    __device__ __forceinline__ void scan(const LinArgs& p, int g0, int lane)
+    {
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
             const int g = g0 + 4 * lane + i;
@@ -52,61 +52,101 @@ __device__ __forceinline__ bool find_rows(const LinArgs& p, int tm, int lane, Li
             const int lo = i ? at[i - 1] : 0;
             at[i] = at[i] < lo ? lo : at[i] > p.rows ? p.rows : at[i];
         }
+        sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             n[i] = (at[i + 1] - at[i] + BM - 1) / BM;
             sum += n[i];
         }
-        int inc = sum;
+        inc = sum;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int x = __shfl_up(inc, d);
             inc += lane >= d ? x : 0;
         }
-        const uint64_t past = __ballot(before + inc > tm);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            int first = before + inc - sum, lo = at[0], hi = at[1], e = g0 + 4 * lane;
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-                if (tm >= first + n[i - 1] && e == g0 + 4 * lane + i - 1) {
-                    first += n[i - 1];
-                    lo = at[i];
-                    hi = at[i + 1];
-                    ++e;
-                }
-            it.e = __builtin_amdgcn_readfirstlane(__shfl(e, l));
-            it.m0 = __builtin_amdgcn_readfirstlane(__shfl(lo + (tm - first) * BM, l));
-            it.end = __builtin_amdgcn_readfirstlane(__shfl(hi, l));
-            it.zero = it.e == p.groups;
-            return true;
-        }
-        before += __shfl(inc, 63);
     }
-    return false;
+    __device__ __forceinline__ int tiles() const { return __builtin_amdgcn_readlane(inc, 63); }
+    // tile tm of this round's (0 <= tm < tiles())
+    __device__ __forceinline__ void find(const LinArgs& p, int g0, int tm, int lane, LinItem& it) const
+    {
+        const int l = __builtin_ctzll(__ballot(inc > tm));
+        int first = inc - sum, lo = at[0], hi = at[1], e = g0 + 4 * lane;
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            if (tm >= first + n[i - 1] && e == g0 + 4 * lane + i - 1) {
+                first += n[i - 1];
+                lo = at[i];
+                hi = at[i + 1];
+                ++e;
+            }
+        it.e = __builtin_amdgcn_readfirstlane(__shfl(e, l));
+        it.m0 = __builtin_amdgcn_readfirstlane(__shfl(lo + (tm - first) * BM, l));
+        it.end = __builtin_amdgcn_readfirstlane(__shfl(hi, l));
+        it.zero = it.e == p.groups;
+    }
+};
+
+// By rows, the grid is the most tiles there could be; the ones there are go
+// to the XCDs in equal, contiguous shares (shares of the grid would leave
+// whole XCDs without work: 1.2 times the time at 32 experts of about 512
+// rows).  False where this work-group has none.
+template <int BM>
+__device__ __forceinline__ bool lin_item_rows(const LinArgs& p, int lane, LinItem& it)
+{
+    RowTiles<BM> round;
+    round.scan(p, 0, lane);
+    int tiles = round.tiles();
+    for (int g0 = 256; g0 <= p.groups; g0 += 256) {
+        RowTiles<BM> more;
+        more.scan(p, g0, lane);
+        tiles += more.tiles();
+    }
+    const int work = tiles * p.tiles_n;
+    const int x = blockIdx.x % kNumXcd, i = blockIdx.x / kNumXcd;
+    const int share = work / kNumXcd, extra = work % kNumXcd;
+    if (i >= share + (x < extra ? 1 : 0))
+        return false;
+    const TileCoord tc = decode_work(x * share + (x < extra ? x : extra) + i, tiles, p.tiles_n, 1, p.group_n);
+    it.tn = tc.tn;
+    it.ks = 0;
+    int tm = tc.tm, g0 = 0;
+    while (tm >= round.tiles()) {       // past the first 256 experts
+        tm -= round.tiles();
+        g0 += 256;
+        round.scan(p, g0, lane);
+    }
+    round.find(p, g0, tm, lane, it);
+    return true;
 }
 
 template <int BM>
 __device__ __forceinline__ bool lin_item(const LinArgs& p, int lane, LinItem& it)
 {
-    const int w = remap_block(blockIdx.x, gridDim.x);
     it.k0 = 0;
     it.steps = p.K / kBK;
     it.zero = false;
     it.e = 0;
     it.end = p.rows;
-    int rest = w;
+    if (p.mode == kByRows)
+        return lin_item_rows<BM>(p, lane, it);
+    int w = remap_block(blockIdx.x, gridDim.x);
     if (p.mode == kByInner) {
-        const int per = p.tiles_m * p.tiles_n;
-        it.e = w / per;
-        rest = w - it.e * per;
+        // Each XCD has an equal share of the tiles, of every expert: their
+        // inner ranges differ, so whole experts would be unequal shares.
+        // Within it expert after expert, whose operands it then shares.
+        const int tiles = p.tiles_m * p.tiles_n, share = (tiles + kNumXcd - 1) / kNumXcd;
+        const int x = blockIdx.x % kNumXcd, i = blockIdx.x / kNumXcd;
+        it.e = i / share;
+        w = x * share + i % share;
+        if (w >= tiles || it.e >= p.groups)
+            return false;
         int lo = p.offsets[it.e], hi = p.offsets[it.e + 1];
         lo = lo < 0 ? 0 : lo > p.K ? p.K : lo;
         hi = hi < lo ? lo : hi > p.K ? p.K : hi;
         it.k0 = lo / kBK;
         it.steps = hi / kBK - it.k0;
     }
-    const TileCoord tc = decode_work(rest, p.tiles_m, p.tiles_n, p.split, p.group_n);
+    const TileCoord tc = decode_work(w, p.tiles_m, p.tiles_n, p.split, p.group_n);
     it.tn = tc.tn;
     it.m0 = tc.tm * BM;
     it.ks = tc.ks;
@@ -115,8 +155,6 @@ __device__ __forceinline__ bool lin_item(const LinArgs& p, int lane, LinItem& it
         it.k0 = tc.ks * share + (tc.ks < more ? tc.ks : more);
         it.steps = share + (tc.ks < more ? 1 : 0);
     }
-    if (p.mode == kByRows)
-        return find_rows<BM>(p, tc.tm, lane, it);
     return true;
 }
 

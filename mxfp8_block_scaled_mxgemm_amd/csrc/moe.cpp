@@ -328,7 +328,11 @@ int plan_linear(mxg::LinArgs* a, int cfg, int cus, int64_t workspace_bytes)
     if (a->mode == mxg::kByRows)    // every expert, and the rows of none, may end inside a tile
         tiles_m = a->rows / t.tile_m + (a->groups + 1 < a->rows ? a->groups + 1 : a->rows);
     const int64_t tiles_n = ((int64_t)a->N + t.tile_n - 1) / t.tile_n;
-    const int64_t work = tiles_m * tiles_n * a->split * (a->mode == mxg::kByInner ? a->groups : 1);
+    int64_t work = tiles_m * tiles_n * a->split;
+    if (a->mode == mxg::kByInner)   // equal shares of the tiles for the XCDs, of every expert
+        work = (work + mxg::kNumXcd - 1) / mxg::kNumXcd * mxg::kNumXcd * a->groups;
+    else if (a->mode == mxg::kByRows)
+        work = (work + mxg::kNumXcd - 1) / mxg::kNumXcd * mxg::kNumXcd;
     if (work >= (1LL << 31))
         return fail(MXGEMM_EUNSUPPORTED, "too many work items");
     a->tiles_m = (int)tiles_m;
