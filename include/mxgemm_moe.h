@@ -10,7 +10,8 @@
  * keeps nothing between calls, can be captured into a HIP graph and may run
  * concurrently with any other.  All pointers are device memory (or memory the
  * GPU can access; anything else is refused with MXGEMM_EINVAL) and must stay
- * valid until the work completes; buffer sizes are the caller's contract.
+ * valid until the work completes; buffer sizes are the caller's contract, and
+ * so is that no output overlaps another operand.
  * Results do not depend on timing: no sum is formed by atomics.
  *
  * MXFP8 here is as in mxgemm_seg.h: FP8 codes (E4M3 or E5M2) in blocks of 32

@@ -114,6 +114,27 @@ def test_dispatch_mx_non_finite_is_the_quantisers():
     assert s[0, 0] == 255 and bool((q[0, :32] == 0x7F).all()) and s[0, 1] == 254 and q[0, 40] == 0x7E
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_dispatch_mx_codes_are_the_quantisers(fmt):
+    """Every finite bfloat16 value, beside its neighbours and beside random
+    others, and random float32 bit patterns: the same codes and scales as the
+    quantiser's."""
+    torch_cuda()
+    bits = torch.arange(1 << 16, dtype=torch.int32)
+    bits = bits[(bits & 0x7F80) != 0x7F80].short()
+    g = torch.Generator().manual_seed(2)
+    n = bits.numel() // 32 * 32
+    wild = torch.randint(-(1 << 31), 1 << 31, (1 << 20,), generator=g, dtype=torch.int64).int().view(torch.float32)
+    tame = torch.randn(1 << 20, generator=g) * torch.exp2(torch.randint(-20, 20, (1 << 20,), generator=g).float())
+    for x in (bits[:n].view(torch.bfloat16).float(), bits[torch.randperm(bits.numel(), generator=g)[:n]].view(
+            torch.bfloat16).float(), wild, tame):
+        x = x.view(-1, 128 if x.numel() % 128 == 0 else 32).cuda()
+        sort = _sorted(torch.zeros(x.shape[0], 1, dtype=torch.int32), 1)
+        q, s = pkg.dispatch_tokens_mx(x, sort, fmt=fmt)
+        rq, rs = pkg.quantize_mxfp8(x, fmt=pkg.FMT_E5M2 if fmt == "e5m2" else pkg.FMT_E4M3)
+        assert torch.equal(s, rs) and torch.equal(q, rq)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("weighted,residual", [(True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("T,k,E,H,drop", CASES)
