@@ -182,7 +182,12 @@ int check_stride(const char* name, int64_t ld, int64_t cols)
 // than half of the compute units (1024 x 2048 x 4096, 128 tiles: 35 against 31
 // us with 64 x 64 ones, exact).  Native dense products of a long K take 256 x
 // 256 tiles, which ask the L2 for half the bytes: 8192 x 8192 x 8192, 485
-// against 584 us; x 2048, 163 against 169; x 512, 88 against 71.
+// against 584 us; x 2048, 163 against 169; x 512, 88 against 71.  By expert
+// they need rows enough to end few tiles early and four tiles per compute
+// unit, since one work-group has it whole: 32 experts of 2048 rows, 4096 x
+// 4096, 1269 against 1427 us; of 1024 rows, 668 against 742, and 386 against
+// 400 at K 2048; of 512 rows, 397 against 395, 244 against 225 at K 2048; 4
+// experts of 2048 rows, 185 against 171.
 int choose_tile(const mxg::LinArgs& a, bool exact, int cus)
 {
     const bool by = a.mode == mxg::kByRows;
@@ -194,7 +199,8 @@ int choose_tile(const mxg::LinArgs& a, bool exact, int cus)
     auto tiles = [&](int64_t m, int64_t n) {
         return (a.mode == mxg::kDense ? 1 : a.groups) * ((r + m - 1) / m) * ((a.N + n - 1) / n);
     };
-    if (!exact && a.mode == mxg::kDense && tiles(256, 256) >= cus && a.K >= 2048)
+    if (!exact && a.K >= 2048 && (a.mode == mxg::kDense ? tiles(256, 256) >= cus
+                                                        : by && r >= 1024 && tiles(256, 256) >= 4 * cus))
         return mxg::kLin256x256;
     return tiles(128, 128) > cus / 2 ? mxg::kLin128x128 : mxg::kLin64x64;
 }
@@ -583,8 +589,9 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
         return fail(MXGEMM_EINVAL, "ld_qt %lld must be a multiple of 128 (%lld where not by expert)",
                     (long long)ld_qt, (long long)padded);
     const int64_t chunks = ld_qt / 128;
-    if (chunks > 65535)
-        return fail(MXGEMM_EUNSUPPORTED, "%lld chunks of 128 tokens exceed 65535", (long long)chunks);
+    if (chunks > 65535 || experts > 65535)
+        return fail(MXGEMM_EUNSUPPORTED, "%lld chunks of 128 tokens or %d experts exceed 65535", (long long)chunks,
+                    experts);
     TRY(check_stride("d_out", ld_d_out, gated ? N / 2 : N));
     if (z)
         TRY(check_stride("z", ld_z, N));

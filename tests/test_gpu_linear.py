@@ -357,6 +357,53 @@ def test_linear_backward(M, N, K, act, gated, by, precision):
             mc.assert_within(atv[:, k0:k_offsets[e + 1]], xe, mc.mx_bound(xe, xe.abs() * 0, "e4m3"), "at")
 
 
+@pytest.mark.parametrize("precision", ["exact", "native"])
+@pytest.mark.parametrize("cfg", [-1, 1, 4])
+@pytest.mark.parametrize("E", [256, 257, 600, 1024])
+def test_by_many_experts(E, cfg, precision):
+    """More experts than one round of the row tiles' list holds; most of them
+    have no row."""
+    torch_cuda()
+    ids = mc.ids_of(torch.Generator().manual_seed(E), 150, 2, E, 0.05)
+    ids[::7, 0] = E - 1
+    _grouped(ids, E, 64, 128, "silu", True, torch.bfloat16, precision, cfg)
+
+
+@pytest.mark.parametrize("E", [300, 1024])
+def test_backward_by_many_experts(E):
+    torch_cuda()
+    M, N, K = 500, 64, 128
+    say(f"linear backward by expert M={M} N={N} K={K} E={E}")
+    g = torch.Generator().manual_seed(E)
+    ids = mc.ids_of(g, M, 1, E, 0.05)
+    sort = pkg.sort_tokens(ids.cuda(), E)
+    offsets, k_offsets = mc.order(ids, E)[:2]
+    x, d = torch.randn(M, K, generator=g).bfloat16(), torch.randn(M, N, generator=g).bfloat16()
+    at, at_s = pkg.quantize_transposed(x.cuda(), sort)
+    wt = torch.randint(0x30, 0x40, (E, K, 128), generator=g, dtype=torch.uint8)
+    wt_s = torch.full((E, K, 4), 127, dtype=torch.uint8)
+    got = pkg.linear_backward(d.cuda(), None, at, at_s, wt.cuda(), wt_s.cuda(), sort=sort)
+    (q, s), (qt, st), db = pkg.epilogue_backward(d.cuda(), sort=sort)
+    assert torch.equal(db, got.d_bias)
+    rows, cols = mc.value(q.cpu(), s.cpu(), "e4m3"), mc.value(qt.cpu(), st.cpu(), "e4m3")
+    atv, wtv = mc.value(at.cpu(), at_s.cpu(), "e4m3"), mc.value(wt, wt_s, "e4m3")
+    da, ta = torch.zeros(M, K, dtype=torch.float64), torch.zeros(M, K, dtype=torch.float64)
+    dw, tw = torch.zeros(E, N, K, dtype=torch.float64), torch.zeros(E, N, K, dtype=torch.float64)
+    rdb, tdb = torch.zeros(E, N, dtype=torch.float64), torch.zeros(E, N, dtype=torch.float64)
+    for e in range(E):
+        lo, hi, k0, k1 = offsets[e], offsets[e + 1], k_offsets[e], k_offsets[e + 1]
+        if hi > lo:
+            for ref, t, at_, u, v in ((da, ta, slice(lo, hi), rows[lo:hi], wtv[e]),
+                                      (dw, tw, e, cols[:, k0:k1], atv[:, k0:k1])):
+                ref[at_] = u @ v.t()
+                t[at_] = mc.product_error(u.abs() @ v.abs().t(), u.shape[1], "exact")
+            rdb[e] = d[lo:hi].double().sum(0)
+            tdb[e] = (hi - lo + 8) * 2.0 ** -24 * d[lo:hi].double().abs().sum(0)
+    for what, out, ref, t in (("d_a", got.d_a, da, ta), ("d_w", got.d_w, dw, tw)):
+        mc.assert_within(out, ref, t + mc.rounding(ref.abs() + t, torch.bfloat16), what)
+    mc.assert_within(db, rdb, tdb, "d_bias")
+
+
 def test_no_tokens():
     torch_cuda()
     u8 = dict(dtype=torch.uint8, device="cuda")
