@@ -85,10 +85,14 @@ def _load():
     return _bound
 
 
-@functools.lru_cache(maxsize=None)
-def _types():
+torch = None        # bound by the first call: the package loads without it
+_TYPES = {}
+
+
+def _bind():
+    global torch
     import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    _TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
 
 
 def _on_stream(fn):
@@ -96,9 +100,10 @@ def _on_stream(fn):
     allocates belongs to that stream, and records its inputs there."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
+        if torch is None:
+            _bind()
         if stream is None:
             return fn(*args, **kw)
-        import torch
         if stream == torch.cuda.current_stream(stream.device):
             with torch.cuda.device(stream.device):
                 return fn(*args, **kw)
@@ -114,9 +119,8 @@ def _on_stream(fn):
 
 def _run(fn, device, *args):
     """fn(*args, stream) on ``device`` and its current stream."""
-    import torch
     i = device.index
-    if i == torch.cuda.current_device():
+    if i == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(i):
@@ -127,7 +131,6 @@ def _run(fn, device, *args):
 
 def _rows_of(t, name, device=None, dtypes=None, shape=None):
     """A device matrix with contiguous rows -> its row stride."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a device tensor")
     if device is not None and t.device != device:
@@ -146,7 +149,6 @@ def _rows_of(t, name, device=None, dtypes=None, shape=None):
 
 
 def _plain(t, name, device, dtype, shape):
-    import torch
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise TypeError(f"{name}: expected a tensor on {device}")
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
@@ -178,7 +180,6 @@ def _up(n, m):
 def sort_tokens(expert_ids, num_experts: int) -> TokenSort:
     """Stable order by expert of the pairs of ``expert_ids`` [T, k] (int32 or
     int64); an id outside [0, num_experts) drops its pair."""
-    import torch
     ids = expert_ids
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
         raise TypeError("expert_ids: expected a device tensor")
@@ -196,16 +197,16 @@ def sort_tokens(expert_ids, num_experts: int) -> TokenSort:
     # one allocation: the four arrays, each from a 16-byte boundary, and the workspace
     e4, n4 = _up(E1, 4), _up(n, 4)
     mem = torch.empty(2 * e4 + 2 * n4 + work // 4, dtype=torch.int32, device=ids.device)
+    offsets, _, k_offsets, _, row_of, _, pair_of, _ = mem.split_with_sizes(
+        (E1, e4 - E1, E1, e4 - E1, n, n4 - n, n, n4 - n + work // 4))
     p = mem.data_ptr()
     _run(lib.mxgemm_sort_tokens, ids.device, ids.data_ptr(), ids.element_size(), T, k, E1 - 1, p, p + 4 * e4,
          p + 8 * e4, p + 8 * e4 + 4 * n4, p + 8 * e4 + 8 * n4, work)
-    row = 2 * e4
-    return TokenSort(mem[:E1], mem[e4:e4 + E1], mem[row:row + n].view(T, k), mem[row + n4:row + n4 + n])
+    return TokenSort(offsets, k_offsets, row_of.view(T, k), pair_of)
 
 
 def _sort_args(sort, device, T=None):
     """(offsets pointer, experts, row_of pointer, T, k) of a TokenSort."""
-    import torch
     offsets, _, row_of, _ = sort
     if row_of.dim() != 2 or offsets.dim() != 1 or (T is not None and row_of.shape[0] != T):
         raise ValueError(f"sort: row_of {tuple(row_of.shape)} is not [tokens{'' if T is None else f' = {T}'}, choices]")
@@ -219,12 +220,11 @@ def _sort_args(sort, device, T=None):
 def dispatch_tokens(x, sort: TokenSort):
     """Rows [T k, H] of the sorted order from tokens x [T, H] (bfloat16,
     float16 or float32); rows of dropped pairs are zero."""
-    import torch
-    ld = _rows_of(x, "x", dtypes=_types())
+    ld = _rows_of(x, "x", dtypes=_TYPES)
     T, H = x.shape
     off, E, row_of, T, k = _sort_args(sort, x.device, T)
     rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-    _run(_load().mxgemm_dispatch_tokens, x.device, x.data_ptr(), ld, _types()[x.dtype], T, k, H, off, E, row_of,
+    _run(_load().mxgemm_dispatch_tokens, x.device, x.data_ptr(), ld, _TYPES[x.dtype], T, k, H, off, E, row_of,
          rows.data_ptr(), H)
     return rows
 
@@ -233,15 +233,14 @@ def dispatch_tokens(x, sort: TokenSort):
 def dispatch_tokens_mx(x, sort: TokenSort, fmt="e4m3"):
     """As dispatch_tokens, quantised to MXFP8: (codes [T k, H], scales [T k,
     H / 32]), both uint8; H a multiple of 32."""
-    import torch
-    ld = _rows_of(x, "x", dtypes=_types())
+    ld = _rows_of(x, "x", dtypes=_TYPES)
     T, H = x.shape
     if H % 32:
         raise ValueError(f"{H} columns are not a multiple of the MX block 32")
     off, E, row_of, T, k = _sort_args(sort, x.device, T)
     q = torch.empty((T * k, H), dtype=torch.uint8, device=x.device)
     s = torch.empty((T * k, H // 32), dtype=torch.uint8, device=x.device)
-    _run(_load().mxgemm_dispatch_tokens_mx, x.device, x.data_ptr(), ld, _types()[x.dtype], T, k, H, off, E, row_of,
+    _run(_load().mxgemm_dispatch_tokens_mx, x.device, x.data_ptr(), ld, _TYPES[x.dtype], T, k, H, off, E, row_of,
          q.data_ptr(), s.data_ptr(), _format(fmt))
     return q, s
 
@@ -251,8 +250,7 @@ def combine_tokens(rows, sort: TokenSort, weights=None, residual=None):
     """Tokens back from their rows: residual[t] + sum_j weights[t, j]
     rows[row_of[t, j]] over the kept pairs, in FP32, rounded once.  rows [T k,
     H]; weights float32 [T, k] (default ones); residual [T, H] of rows' type."""
-    import torch
-    ld = _rows_of(rows, "rows", dtypes=_types())
+    ld = _rows_of(rows, "rows", dtypes=_TYPES)
     off, E, row_of, T, k = _sort_args(sort, rows.device)
     n, H = rows.shape
     if n != T * k:
@@ -260,7 +258,7 @@ def combine_tokens(rows, sort: TokenSort, weights=None, residual=None):
     w = None if weights is None else _plain(weights, "weights", rows.device, torch.float32, (T, k))
     ld_res = 0 if residual is None else _rows_of(residual, "residual", rows.device, (rows.dtype,), (T, H))
     out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
-    _run(_load().mxgemm_combine_tokens, rows.device, rows.data_ptr(), ld, _types()[rows.dtype], T, k, H, off, E,
+    _run(_load().mxgemm_combine_tokens, rows.device, rows.data_ptr(), ld, _TYPES[rows.dtype], T, k, H, off, E,
          row_of, w, None if residual is None else residual.data_ptr(), ld_res, out.data_ptr(), H)
     return out
 
@@ -274,8 +272,7 @@ def dispatch_tokens_backward(d_rows, sort: TokenSort, stream=None):
 def combine_tokens_backward(d_out, rows, sort: TokenSort, weights=None):
     """Gradients of combine_tokens to its rows ([T k, H] of rows' type) and
     weights (float32 [T, k]); the residual's is d_out itself."""
-    import torch
-    ld = _rows_of(rows, "rows", dtypes=_types())
+    ld = _rows_of(rows, "rows", dtypes=_TYPES)
     off, E, row_of, T, k = _sort_args(sort, rows.device)
     n, H = rows.shape
     if n != T * k:
@@ -285,7 +282,7 @@ def combine_tokens_backward(d_out, rows, sort: TokenSort, weights=None):
     d_rows = torch.empty((n, H), dtype=rows.dtype, device=rows.device)
     d_w = torch.empty((T, k), dtype=torch.float32, device=rows.device)
     _run(_load().mxgemm_combine_tokens_backward, rows.device, d_out.data_ptr(), ld_d, rows.data_ptr(), ld,
-         _types()[rows.dtype], T, k, H, off, E, row_of, w, d_rows.data_ptr(), H, d_w.data_ptr())
+         _TYPES[rows.dtype], T, k, H, off, E, row_of, w, d_rows.data_ptr(), H, d_w.data_ptr())
     return d_rows, d_w
 
 
@@ -294,11 +291,13 @@ def combine_tokens_backward(d_out, rows, sort: TokenSort, weights=None):
 def _laid_out(t):
     """``t``, or where its other axis is the contiguous one (a transposed view)
     a copy with contiguous rows; [.., N, K] bytes."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.uint8 or not 2 <= t.dim() <= 3:
-        return t            # refused by the checks that follow
-    stride, shape = t.stride(), t.shape
-    if stride[-1] == 1 or shape[-1] <= 1 or stride[-2] != 1 or stride[-1] < shape[-2]:
+    if torch is None:
+        _bind()
+    stride = t.stride() if isinstance(t, torch.Tensor) else ()
+    if not 2 <= len(stride) <= 3 or stride[-1] == 1 or t.dtype != torch.uint8 or not t.is_cuda:
+        return t            # as it should be, or refused by the checks that follow
+    shape = t.shape
+    if shape[-1] <= 1 or stride[-2] != 1 or stride[-1] < shape[-2]:
         return t
     out = torch.empty(shape, dtype=torch.uint8, device=t.device)
     _run(_load().mxgemm_transpose_bytes, t.device, t.data_ptr(), stride[-1], stride[0] if len(shape) == 3 else 0,
@@ -308,7 +307,6 @@ def _laid_out(t):
 
 def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, out_dtype, preact, precision, a_fmt,
             w_fmt, tile_cfg):
-    import torch
     u8 = (torch.uint8,)
     a, a_scale, w, w_scale = _laid_out(a), _laid_out(a_scale), _laid_out(w), _laid_out(w_scale)
     lda = _rows_of(a, "a", dtypes=u8)
@@ -333,7 +331,7 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         raise ValueError(f"a gated product needs an even N, not {N}")
     cols = N // 2 if gated else N
     mx = isinstance(out_dtype, str)
-    if mx and out_dtype not in _MX_OUT or not mx and out_dtype not in _types():
+    if mx and out_dtype not in _MX_OUT or not mx and out_dtype not in _TYPES:
         raise ValueError(f"out_dtype {out_dtype!r} is not a 16- or 32-bit float type, 'e4m3' or 'e5m2'")
     if mx and cols % 32:
         raise ValueError(f"MXFP8 output needs columns in blocks of 32, not {cols}")
@@ -341,10 +339,10 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         raise ValueError(f"unknown precision mode {precision!r}")
     bias_ptr = res_ptr = scale_ptr = z_ptr = ld_res = bias_type = 0
     if bias is not None:
-        if bias.dtype not in _types():
+        if bias.dtype not in _TYPES:
             raise TypeError(f"bias: {bias.dtype} is not a 16- or 32-bit float type")
         bias_ptr = _plain(bias, "bias", dev, bias.dtype, (E, N) if by_row else (N,))
-        bias_type = _types()[bias.dtype]
+        bias_type = _TYPES[bias.dtype]
     if residual is not None:
         ld_res = _rows_of(residual, "residual", dev, (torch.bfloat16 if mx else out_dtype,), (M, cols))
         res_ptr = residual.data_ptr()
@@ -370,7 +368,7 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias_ptr, res_ptr, out.data_ptr(),
         scale_ptr, z_ptr, off, M, N, K, lda, lda_s, ldw, ldw_s, w_group, w_scale_group, ld_res, cols, M * cols,
         cols // 32, N, mode, E, _format(a_fmt), _format(w_fmt), _PRECISION[precision], bias_type, _activation(act),
-        1 if gated else 0, _MX_OUT[out_dtype] if mx else _types()[out_dtype], tile_cfg, work_ptr, work))
+        1 if gated else 0, _MX_OUT[out_dtype] if mx else _TYPES[out_dtype], tile_cfg, work_ptr, work))
     return result[0] if len(result) == 1 else tuple(result)
 
 
@@ -389,7 +387,6 @@ def linear(a, a_scale, w, w_scale, bias=None, act="none", gated=False, residual=
     MXFP8 codes and scales, ready for the next product.  precision: "exact" or
     "native", as for SegGemm.  Returns out, or a tuple of out, its scales
     (MXFP8) and z in bfloat16 (``preact``, for linear_backward)."""
-    import torch
     return _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets,
                    GROUP_NONE if offsets is None else GROUP_ROWS, torch.bfloat16 if out_dtype is None else out_dtype,
                    preact, precision, a_fmt, w_fmt, tile_cfg)
@@ -400,7 +397,6 @@ def linear_by_inner(a, a_scale, w, w_scale, offsets, out_dtype=None, precision="
                     tile_cfg=-1):
     """[E, M, N] products a w^T over the inner ranges offsets[e] ..
     offsets[e + 1] (TokenSort.k_offsets): the weights' gradient by expert."""
-    import torch
     return _linear(a, a_scale, w, w_scale, None, "none", False, None, offsets, GROUP_INNER,
                    torch.bfloat16 if out_dtype is None else out_dtype, False, precision, a_fmt, w_fmt, tile_cfg)
 
@@ -408,9 +404,8 @@ def linear_by_inner(a, a_scale, w, w_scale, offsets, out_dtype=None, precision="
 def _epilogue_backward(d_out, z, act, gated, sort, fmt, rows, cols, bias):
     """(q, s), (qt, st), d_bias of mxgemm_epilogue_backward; None where not
     asked for."""
-    import torch
     dev = d_out.device
-    ld_d = _rows_of(d_out, "d_out", dtypes=_types())
+    ld_d = _rows_of(d_out, "d_out", dtypes=_TYPES)
     M = d_out.shape[0]
     N = d_out.shape[1] * (2 if gated else 1)
     ld_z = 0 if z is None else _rows_of(z, "z", dev, (torch.bfloat16,), (M, N))
@@ -433,7 +428,7 @@ def _epilogue_backward(d_out, z, act, gated, sort, fmt, rows, cols, bias):
         db = torch.empty((E, N) if E else (N,), dtype=torch.float32, device=dev)
         work = torch.empty((ld_qt // STEP, N), dtype=torch.float32, device=dev)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _run(_load().mxgemm_epilogue_backward, dev, d_out.data_ptr(), _types()[d_out.dtype], ld_d, ptr(z), ld_z, M, N,
+    _run(_load().mxgemm_epilogue_backward, dev, d_out.data_ptr(), _TYPES[d_out.dtype], ld_d, ptr(z), ld_z, M, N,
          _activation(act), 1 if gated else 0, off or None, koff or None, E, _format(fmt), ptr(q), ptr(s), ptr(qt),
          ptr(st), ld_qt, ptr(db), ptr(work), 0 if work is None else work.numel() * 4)
     return (q, s), (qt, st), db
@@ -472,7 +467,6 @@ def linear_backward(d_out, z, at, at_scale, wt, wt_scale, act="none", gated=Fals
     quantize_transposed(.., sort); d_w is [E, N, K], d_bias [E, N], and
     dropped rows of d_a are zero.  d_a and d_w are of ``out_dtype`` (default
     bfloat16), d_bias float32."""
-    import torch
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if isinstance(out_dtype, str):
         raise ValueError("gradients are not written in MXFP8")
