@@ -10,7 +10,8 @@ namespace mxg {
 // bytes per column, so LDS and the stores move words and 16-byte pieces.  In
 // LDS a column's eight 16-byte pieces are XOR-swizzled by bits 4-6 of the
 // column: the eight threads that write columns 16 apart meet different banks.
-// Bound by memory: every byte read and written once.
+// Bound by memory, every byte read and written once: 24 x 2048 x 2048, 35 us
+// (201 MB, 5.7 TB/s); 7168 x 4096, 15 us.
 constexpr int kTurn = 128;
 
 // Word w of column c.

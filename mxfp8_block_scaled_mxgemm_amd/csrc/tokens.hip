@@ -229,7 +229,9 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t stream)
 //
 // One thread per piece of V elements of a token: read once, written to the
 // rows of the token's k pairs (zero where the pair was dropped).  Bound by
-// memory: tokens * cols read, tokens * k * cols written.
+// memory: tokens * cols read, tokens * k * cols written.  Measured: 5001 x 2047
+// FP16 to 6 rows each, 42 us (143 MB, 3.4 TB/s: rows of odd length, so most
+// 16-byte pieces lie across two lines).
 
 // Kept rows, within the rows there are.
 __device__ __forceinline__ int live_rows(const TokenArgs& p)
@@ -284,6 +286,8 @@ __global__ void __launch_bounds__(256) dispatch_kernel(TokenArgs p, int pieces)
 // To MXFP8: two threads per block of 32, sixteen elements each; quantised
 // once per token, the codes and scale byte written k times.  The rules are
 // the quantiser's (a NaN makes the block's scale 0xFF and its codes 0x7F).
+// Bound by memory: 8192 x 4096 bfloat16 to 8 rows each, 69 us (344 MB, 5.0
+// TB/s; a large copy reaches 4.9).
 template <int TYPE, int F>
 __global__ void __launch_bounds__(256) dispatch_mx_kernel(TokenArgs p, int pieces)
 {
@@ -333,7 +337,8 @@ __global__ void __launch_bounds__(256) dispatch_mx_kernel(TokenArgs p, int piece
 // summed in FP32 and rounded once; dropped pairs add nothing (whatever their
 // weight holds).  One thread per piece; eight rows' loads are in flight at a
 // time.  Bound by memory.  The gradient of dispatch is the same sum with all
-// weights one.
+// weights one.  Measured: 8192 x 4096 bfloat16 from 8 rows each and a
+// residual, 155 us (671 MB, 4.3 TB/s); one token 3.8 us.
 template <int TYPE, int V>
 __global__ void __launch_bounds__(256) combine_kernel(TokenArgs p, int pieces)
 {
@@ -394,7 +399,8 @@ __global__ void __launch_bounds__(256) combine_kernel(TokenArgs p, int pieces)
 // takes pieces threadIdx.x, + blockDim.x, ... of d_out and, for eight pairs
 // at a time, the same pieces of their rows, so d_out is read once and every
 // row once.  The partial dots are added over the lanes and then over the
-// waves, in a fixed order.
+// waves, in a fixed order.  Bound by memory: 8192 x 4096 bfloat16, 8 rows
+// each, 276 us (1.14 GB, 4.1 TB/s).
 template <int TYPE, int V>
 __global__ void __launch_bounds__(256) combine_backward_kernel(TokenArgs p, int pieces)
 {
