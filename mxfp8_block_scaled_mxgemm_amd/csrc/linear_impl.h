@@ -632,19 +632,27 @@ __device__ __forceinline__ T& pick(T& a, T& b)
         return b;
 }
 
+// Task i where c tasks 0 .. c - 1 and r tasks c .. c + r - 1 take turns.
+constexpr int take_turns(int i, int c, int r)
+{
+    const int both = 2 * (c < r ? c : r);
+    return i < both ? (i & 1 ? c + i / 2 : i / 2) : c < r ? i : i - r;
+}
+
 // K loop on the scaled FP8 MFMA (32 x 32 x 64), software-pipelined.  A
 // K-step (128 K) is two sub-steps m of 64 K.  While the GA x GB MFMAs of a
 // sub-step run, the fragments of the next one are read from LDS into the
 // other register set, so no MFMA waits for a read.  The one barrier of a
-// K-step opens sub-step 1: by then step s + 1 has landed and every wave holds
-// all of step s in registers, so the copies of step s + 2 are issued into its
-// stage at once and have a whole K-step to land.  Large wave tiles
+// K-step comes three quarters through sub-step 0: by then step s + 1 has
+// landed and every wave holds all of step s in registers, so the copies of
+// step s + 2 are issued into its stage at once and have a whole K-step to
+// land.  (8192 x 8192 x 8192: 466 us; with the barrier between the sub-steps
+// 474, and there with all copies before the fragments' reads 486.)  Large wave tiles
 // keep the LDS reads per MFMA low: a 128 x 128 wave tile reads each byte for
 // 128 outputs, and four of them read 128 KB per 256 x 256 x 128 step (1024
 // clocks at 128 bytes per clock, plus 512 for the copies' writes, against
 // 2048 clocks of MFMA), where eight waves of 128 x 64 read 192 KB.
-// Measured: 8192 x 8192 x 8192 in 256 x 256 tiles 490 us (2.24 PFLOP/s); 450
-// of it is this loop, 1.69 us per K-step, and 389 with the copies taken out.
+// In all 2.36 PFLOP/s, at 2.2 GHz; the MFMAs alone would take 240 us there.
 // Scale bytes: a lane reads the four of its row as one word, shifted so that
 // byte 2 m is its block's in sub-step m.
 // src: sources of the loop's first K-step, of `valid` ones; nsteps: the
@@ -738,30 +746,36 @@ __device__ __forceinline__ void native_mainloop(const LinArgs& p, uint8_t* stage
         uint32_t swn[NF];
         static_for<0, 2>([&](auto mc) __attribute__((always_inline)) {
             constexpr int m = decltype(mc)::value;
-            if constexpr (m == 1) {
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                __syncthreads();
-            }
             const uint8_t* from = m == 0 ? cur : nxt;
             auto& now = pick<m>(fr0, fr1);
             auto& then = pick<1 - m>(fr0, fr1);
-            // the sub-step's other work, in this order: at m = 1 the copies
-            // of step s + 2 and of scale words; the fragments of the next
-            // sub-step; at m = 0 the next K-step's scale words.  At m = 0 it
-            // ends three quarters through, so that the barrier's wait for
-            // the reads has MFMAs to hide behind.
-            constexpr int ncopy = m == 1 ? NC : 0, nscale = m == 1 ? G::JS : 0;
+            // Beside the MFMAs.  m = 0: the fragments of sub-step 1 and the
+            // next K-step's scale words in the first half, so that the
+            // barrier's wait for them is short; after the barrier the first
+            // copies of step s + 2.  m = 1: the other copies and the
+            // next K-step's fragments in turns (the load unit takes about one
+            // copy of each wave per MFMA, and fragments read last would be
+            // waited for).
+            constexpr int kEarly = NU / 4;      // MFMAs, and copies, of sub-step 0 after the barrier
+            constexpr int ncopy = m == 1 ? NC - kEarly : 0, nscale = m == 1 ? G::JS : 0;
             constexpr int reads = ncopy + nscale, words = reads + 2 * NF;
-            constexpr int ntask = words + (m == 0 ? NF : 0), over = m == 0 ? NU - NU / 4 : NU;
+            constexpr int ntask = words + (m == 0 ? NF : 0), over = m == 0 ? NU / 2 : NU;
             static_for<0, NU>([&](auto uc) __attribute__((always_inline)) {
                 constexpr int u = decltype(uc)::value, i = u / GB, g = u % GB;
+                if constexpr (m == 0 && u == NU - kEarly) {
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    __syncthreads();
+                }
                 acc[i][g] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                     operand(now[GA + g]), operand(now[i]), acc[i][g], FB, FA, 2 * m, (int)sw[GA + g], 2 * m, (int)sw[i]);
                 constexpr int t0 = u < over ? u * ntask / over : ntask, t1 = u < over ? (u + 1) * ntask / over : ntask;
+                if constexpr (m == 0 && u >= NU - kEarly)
+                    co.issue(src2, cur, wl, u - (NU - kEarly));
                 static_for<t0, t1>([&](auto tc) __attribute__((always_inline)) {
-                    constexpr int t = decltype(tc)::value;
+                    constexpr int i0 = decltype(tc)::value;
+                    constexpr int t = m == 0 ? i0 : take_turns(i0, reads, 2 * NF);
                     if constexpr (t < ncopy) {
-                        co.issue(src2, cur, wl, t);
+                        co.issue(src2, cur, wl, t + kEarly);
                     } else if constexpr (t < reads) {
                         co.issue_scales(ssrc, next_slot, scales + 2 * G::SCALES, more ? ~0u : 0u, wl, t - ncopy);
                     } else if constexpr (t < words) {
@@ -930,9 +944,9 @@ __device__ __forceinline__ void groups_partial(const LinArgs& p, uint8_t* lds, v
 // free: the accumulators go through LDS in slabs of 32 rows x 64 columns, so
 // that bias, activation, residual and the stores run on whole rows; the K
 // groups' slabs are added there in group order.  Measured, with what bounds
-// them: 256 x 256 native, 8192 x 8192 x 8192 with bias, silu and residual, 505
+// them: 256 x 256 native, 8192 x 8192 x 8192 with bias, silu and residual, 485
 // us (the K loop's copies; the epilogue 5%); 128 x 128 native by expert, 16384
-// rows of 4096 x 4096 over 32 experts, gated silu to MXFP8, 395 us, 1.39
+// rows of 4096 x 4096 over 32 experts, gated silu to MXFP8, 395 us, 1.40
 // PFLOP/s (the same copies, twice the bytes per product, and tiles that end
 // early: 11% of their rows); by inner range, exact, 24 experts of 384 tokens,
 // 2048 x 2048, 135 us (the writes of 201 MB, 60 us, and the K loop at 1.03

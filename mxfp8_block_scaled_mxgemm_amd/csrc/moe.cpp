@@ -181,13 +181,13 @@ int check_stride(const char* name, int64_t ld, int64_t cols)
 // epilogue of one runs beside the K loop of the other), where they occupy more
 // than half of the compute units (1024 x 2048 x 4096, 128 tiles: 35 against 31
 // us with 64 x 64 ones, exact).  Native dense products of a long K take 256 x
-// 256 tiles, which ask the L2 for half the bytes: 8192 x 8192 x 8192, 485
-// against 584 us; x 2048, 163 against 169; x 512, 88 against 71.  By expert
+// 256 tiles, which ask the L2 for half the bytes: 8192 x 8192 x 8192, 472
+// against 592 us; x 2048, 161 against 169; x 512, 93 against 76.  By expert
 // they need rows enough to end few tiles early and four tiles per compute
 // unit, since one work-group has it whole: 32 experts of 2048 rows, 4096 x
-// 4096, 1269 against 1427 us; of 1024 rows, 668 against 742, and 386 against
-// 400 at K 2048; of 512 rows, 397 against 395, 244 against 225 at K 2048; 4
-// experts of 2048 rows, 185 against 171.
+// 4096, 1224 against 1449 us; of 1024 rows, 644 against 757, and 381 against
+// 411 at K 2048; of 512 rows, 393 against 410, 245 against 228 at K 2048; 4
+// experts of 2048 rows, 180 against 178.
 int choose_tile(const mxg::LinArgs& a, bool exact, int cus)
 {
     const bool by = a.mode == mxg::kByRows;
