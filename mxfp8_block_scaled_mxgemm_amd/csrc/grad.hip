@@ -3,6 +3,7 @@
 #include "element.h"
 #include "linear.h"
 #include "quant.h"
+#include "schedule.h"
 
 namespace mxg {
 
@@ -59,17 +60,24 @@ struct Raw16 {
 // thread computes eight columns (FUSED: eight of each half) of a few rows;
 // the loads of all its rows go out before the first is used.  Along the
 // columns, four threads share a block of 32 and quantise it at once.  The
-// FP32 values also go to LDS, transposed to [column][token] and padded so
-// that neither side piles onto a few banks; there a thread takes one column's
-// block of 32 tokens: its sum, its scale, its codes (32 bytes; four threads
-// write one column's 128 bytes).  Tokens past the expert's last one count as
-// zeros, so blocks never cross experts.  Bound by memory: d_out and z are
-// read once and the two bytes per element written: 4096 x 4096 with
-// gelu_tanh, 31 us (103 MB, 3.3 TB/s); 8002 rows of 2 x 1024 gated with silu
-// over 24 experts, 35 us (86 MB, 2.5 TB/s).  What keeps it from the rate of a
-// copy is the arithmetic: two quantisations and the activation's slope per
-// element.
-constexpr int kGradRows = 128, kGradCols = 64, kGradLd = kGradRows + 1;
+// FP32 values also go to LDS, transposed to [column][token]; there a thread
+// takes one column's block of 32 tokens: its sum, its scale, its codes (32
+// bytes; four threads write one column's 128 bytes).  Tokens past the expert's
+// last one count as zeros, so blocks never cross experts.  d_out and z are read
+// once and the two bytes per element written: 4096 x 4096 with gelu_tanh, 31
+// us (103 MB, 3.3 TB/s); 8002 rows of 2 x 1024 gated with silu over 24
+// experts, 31 us (86 MB, 2.8 TB/s).  Bound by instructions: two quantisations
+// and the activation's slope per element.
+constexpr int kGradRows = 128, kGradCols = 64;
+
+// Place of (tile column, row) in LDS: spread so that neither eight columns 8
+// apart of neighbouring rows (the writes) nor eight columns by four blocks of
+// 32 rows (the reads) meet in one of 32 banks.
+constexpr int kGradWords = 132 * kGradCols + 64;
+__device__ __forceinline__ int grad_at(int col, int row)
+{
+    return 132 * col + 8 * (col >> 3) + 4 * (col >> 5) + row + (row >> 5);
+}
 
 // First token of a chunk of 128 and the end of its expert; false past the
 // last segment.
@@ -157,7 +165,19 @@ __device__ __forceinline__ void grad_put(const GradArgs& p, float* t, int row, i
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-        t[(tc + u) * kGradLd + r] = dz[u];
+        t[grad_at(tc, r) + 132 * u] = dz[u];     // tc is a multiple of 8
+}
+
+// FUSED tiles take 64 bytes of a row of d_out: two neighbours share a line, so
+// both go to one XCD (else every line is fetched into two L2s: 94 MB for 49,
+// and 34 us against 31 for the 8002 rows above).
+__device__ __forceinline__ int paired_tile()
+{
+    const int x = blockIdx.x;
+    if (gridDim.x % kNumXcd != 0 || (x | (2 * kNumXcd - 1)) >= (int)gridDim.x)
+        return x;
+    const int i = x % (2 * kNumXcd);
+    return x - i + 2 * (i % kNumXcd) + i / kNumXcd;
 }
 
 // VEC: whole eights of 16-bit d_out (and z) columns, so a row's loads are
@@ -165,14 +185,14 @@ __device__ __forceinline__ void grad_put(const GradArgs& p, float* t, int row, i
 template <int F, bool FUSED, bool VEC>
 __global__ void __launch_bounds__(256) grad_kernel(GradArgs p)
 {
-    __shared__ float t[kGradCols * kGradLd];
+    __shared__ float t[kGradWords];
     const int tid = threadIdx.x, lane = tid & 63;
     const int chunk = blockIdx.y;
     int row0, end;
     if (!grad_rows(p, chunk, row0, end))
         return;
     const int half = p.N / 2;
-    const int n0 = blockIdx.x * kGradCols;      // FUSED: columns n0 / 2 of both halves
+    const int n0 = (FUSED ? paired_tile() : blockIdx.x) * kGradCols;    // FUSED: columns n0 / 2 of both halves
     constexpr int kLanes = FUSED ? 4 : 8;       // threads across the columns
     constexpr int kPasses = kGradRows * kLanes / 256;
     const int cl = tid % kLanes, rl = tid / kLanes;
@@ -243,7 +263,7 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs p)
     const int col = tid >> 2, b = tid & 3;      // column, block of 32 tokens
     const int n = FUSED ? n0 / 2 + (col & 31) + (col >= 32 ? half : 0) : n0 + col;
     const bool there = FUSED ? n0 / 2 + (col & 31) < half : n < p.N;
-    const float* v = t + col * kGradLd + 32 * b;
+    const float* v = t + grad_at(col, 32 * b);
     float x[32], sum = 0.f;
     uint32_t m = 0;
 #pragma unroll
