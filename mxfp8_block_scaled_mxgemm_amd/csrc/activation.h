@@ -74,9 +74,12 @@ __device__ __forceinline__ float activate_grad(int act, float z, float& y)
         return cdf + z * 0.3989422804014327f * __expf(-0.5f * z * z);
     }
     case kActGeluTanh: {
-        const float s = sigmoid(kGeluC * z * (1.f + kGeluA * z * z));
+        // s is 0 or 1 long before |z| = 100; past it z * z may overflow, and
+        // 0 times infinity must not come of it
+        const float zz = fminf(z * z, 1e4f);
+        const float s = sigmoid(kGeluC * z * (1.f + kGeluA * zz));
         y = z * s;
-        return s + z * s * (1.f - s) * kGeluC * (1.f + 3.f * kGeluA * z * z);
+        return s + z * s * (1.f - s) * kGeluC * (1.f + 3.f * kGeluA * zz);
     }
     case kActSilu: {
         const float s = sigmoid(z);

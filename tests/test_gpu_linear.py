@@ -305,6 +305,32 @@ def test_epilogue_gradient_is_the_derivative():
                 mc.assert_within(db[half * N:(half + 1) * N], slope, bound, f"{act} gated={gated} half {half}")
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_large_values(act, gated):
+    """Far out, where squares and cubes pass FP32's range: values and slopes
+    stay those of the limits (z or 0, 1 or 0)."""
+    torch_cuda()
+    v = torch.tensor([64.0, 1e4, 1e10, 1e13, 1e19, 3e19, 1e20, 1e30, 3e38]).bfloat16().float()
+    z = torch.cat([v, -v, torch.zeros(14)])
+    n = z.numel()
+    full = torch.cat([z, torch.ones(n)]) if gated else z
+    zero = _cuda(torch.zeros(1, 128, dtype=torch.uint8), torch.full((1, 4), 127, dtype=torch.uint8))
+    w = _cuda(torch.zeros(full.numel(), 128, dtype=torch.uint8), torch.full((full.numel(), 4), 127, dtype=torch.uint8))
+    out = pkg.linear(*zero, *w, bias=full.cuda(), act=act, gated=gated, out_dtype=torch.float32)
+    ref = mc.act(z.double(), act).view(1, -1)
+    mc.assert_within(out, ref, mc.ACT_ERR * z.double().abs().view(1, -1) + 2.0 ** -126, f"{act} gated={gated}")
+    for pad in (0, 1):      # whole eights, and not
+        d = torch.ones(1, n + pad)
+        fz = torch.cat([torch.nn.functional.pad(x, (0, pad)) for x in full.view(-1, n)]).view(1, -1).bfloat16()
+        _, _, db = pkg.epilogue_backward(d.bfloat16().cuda(), fz.cuda(), act=act, gated=gated)
+        slope = mc.act_grad(z.double(), act)
+        mc.assert_within(db[:n], slope, 64 * 2.0 ** -24 + 0 * slope, f"{act} slope gated={gated}")
+        if gated:
+            mc.assert_within(db[n + pad:2 * n + pad], ref[0], 64 * 2.0 ** -24 * z.double().abs() + 2.0 ** -126,
+                             f"{act} of the gate")
+
+
 @pytest.mark.parametrize("precision", ["exact", "native"])
 @pytest.mark.parametrize("by", [False, True])
 @pytest.mark.parametrize("M,N,K,act,gated", [(96, 128, 256, "none", False), (200, 162, 128, "none", False),
