@@ -131,7 +131,8 @@ enum { MXGEMM_GROUP_NONE = 0,   /* one product                                  
  * K % 128 == 0 (one MFMA K-step), as everywhere in this library.  GROUP_INNER
  * takes no bias, activation, gate, residual or z.
  * Errors: EINVAL, EUNSUPPORTED (K not a multiple of 128; more than 2^31 work
- * items; gated weights of 4 GiB or more per expert), EHIP.
+ * items; gated weights, or their scales, that span 4 GiB or more per expert),
+ * EHIP.
  */
 typedef struct mxgemm_linear {
     const void* a;

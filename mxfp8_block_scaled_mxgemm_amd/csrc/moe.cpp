@@ -276,8 +276,8 @@ int check_linear(const mxgemm_linear_t* g, mxg::LinArgs* a)
     if (g->lda > (1 << 30) / 256 * 2 || g->ldw > (1 << 30) / 256 * 2 || g->ld_a_scale > (1 << 22) ||
         g->ld_w_scale > (1 << 22))
         return fail(MXGEMM_EUNSUPPORTED, "row strides of the operands are limited to 8 MiB (scales 4 MiB)");
-    if (g->gated && (g->N / 2 + 256) * g->ldw >= (1LL << 32))
-        return fail(MXGEMM_EUNSUPPORTED, "gated weights of 4 GiB or more per expert");
+    if (g->gated && ((g->N / 2 + 256) * g->ldw >= (1LL << 32) || (g->N / 2 + 256) * g->ld_w_scale >= (1LL << 32)))
+        return fail(MXGEMM_EUNSUPPORTED, "gated weights (or their scales) of 4 GiB or more per expert");
     memset(a, 0, sizeof(*a));
     a->a = (const uint8_t*)g->a;
     a->as = (const uint8_t*)g->a_scale;

@@ -88,6 +88,7 @@ def _args(**kw):
     (dict(lda=1 << 24), _lib.MXGEMM_EUNSUPPORTED),
     (dict(mode=2, experts=2, offsets=16, act=1), _lib.MXGEMM_EINVAL),
     (dict(gated=1, N=1 << 25, ldw=256, ld_out=1 << 24), _lib.MXGEMM_EUNSUPPORTED),
+    (dict(gated=1, N=1 << 21, ld_w_scale=1 << 22, ld_out=1 << 20), _lib.MXGEMM_EUNSUPPORTED),
 ])
 def test_linear_refuses_before_touching_a_gpu(kw, code):
     lib = _moe._load()
