@@ -172,11 +172,12 @@ int mxgemm_linear(const mxgemm_linear_t* args, void* stream);
  *        [g, u] = z; in FP32 (relu: derivative 0 at 0)
  *   q, s    dz quantised along its columns: codes [rows][Np], scales
  *           [rows][Np/32], Np = N rounded up to 128 (zeros past N); d_a = dz w
- *           is mxgemm_linear of them with w transposed ([K][Np])
+ *           is mxgemm_linear of them with w transposed ([K][Np]); by expert, rows
+ *           of dropped pairs are zero
  *   qt, st  dz transposed and quantised along the tokens: codes [N][ld_qt],
  *           scales [N][ld_qt/32]; by expert, expert e's tokens take columns
- *           [k_offsets[e], k_offsets[e+1]) (zeros past its last token), else
- *           ld_qt is rows rounded up to 128; d_w = dz^T a is mxgemm_linear of
+ *           [k_offsets[e], k_offsets[e+1]) (zeros past its last token, and past
+ *           the last segment), else ld_qt is rows rounded up to 128; d_w = dz^T a is mxgemm_linear of
  *           them with a transposed ([K][ld_qt]), by expert in GROUP_INNER mode
  *           with k_offsets
  *   d_bias  float32 [experts][N] ([N] where not by expert): sums of dz over

@@ -440,7 +440,8 @@ def epilogue_backward(d_out, z=None, act="none", gated=False, sort=None, fmt="e4
     along the columns [M, Np], (qt, st) transposed along the tokens [N, ..],
     d_bias float32); parts not asked for are None.  Np is N rounded up to 128.
     With ``sort`` the tokens of expert e take columns k_offsets[e] ..
-    k_offsets[e + 1] of qt, and d_bias is [E, N]."""
+    k_offsets[e + 1] of qt, and d_bias is [E, N]; rows of dropped pairs and
+    columns past the last segment are zero."""
     return _epilogue_backward(d_out, z, act, gated, sort, fmt, rows, cols, bias)
 
 

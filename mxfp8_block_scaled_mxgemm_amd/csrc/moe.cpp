@@ -589,8 +589,8 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
         return fail(MXGEMM_EINVAL, "ld_qt %lld must be a multiple of 128 (%lld where not by expert)",
                     (long long)ld_qt, (long long)padded);
     const int64_t chunks = ld_qt / 128;
-    if (chunks > 65535 || experts > 65535)
-        return fail(MXGEMM_EUNSUPPORTED, "%lld chunks of 128 tokens or %d experts exceed 65535", (long long)chunks,
+    if (chunks > 65534 || experts > 65535)      // of the grid's second dimension, one for what is past the last
+        return fail(MXGEMM_EUNSUPPORTED, "%lld chunks of 128 tokens or %d experts exceed 65534", (long long)chunks,
                     experts);
     TRY(check_stride("d_out", ld_d_out, gated ? N / 2 : N));
     if (z)

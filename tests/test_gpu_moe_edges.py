@@ -1,0 +1,83 @@
+"""Edges of the expert layer on the GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import mxfp8_block_scaled_mxgemm_amd as pkg
+import moe_common as mc
+from gpu_common import say, torch_cuda
+from mxfp8_block_scaled_mxgemm_amd import _moe
+
+pytestmark = pytest.mark.gpu
+
+
+def _filled(*shape):
+    return torch.full(shape, 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def _pointer(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _grad_abi(d, z, act, gated, sort, fmt, ld_qt, rows=True, cols=True):
+    """mxgemm_epilogue_backward by expert into buffers that hold 0xA5."""
+    M, N = d.shape[0], d.shape[1] * (2 if gated else 1)
+    E, Np = sort.offsets.numel() - 1, -(-N // 128) * 128
+    q, s = (_filled(M, Np), _filled(M, Np // 32)) if rows else (None, None)
+    qt, st = (_filled(N, ld_qt), _filled(N, ld_qt // 32)) if cols else (None, None)
+    rc = _moe._load().mxgemm_epilogue_backward(
+        _pointer(d), _moe._TYPES[d.dtype], d.shape[1], _pointer(z), N, M, N, pkg._moe.ACTIVATIONS[act], int(gated),
+        _pointer(sort.offsets), _pointer(sort.k_offsets), E, pkg._moe._FMT[fmt], _pointer(q), _pointer(s),
+        _pointer(qt), _pointer(st), ld_qt, None, None, 0, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0, pkg.last_error()
+    torch.cuda.synchronize()
+    return q, s, qt, st
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,act,gated,E,drop", [
+    (1, 2, "silu", True, 5, 1.0), (5, 34, "gelu", True, 3, 0.5), (130, 64, "gelu_tanh", False, 5, 0.1),
+    (300, 128, "silu", True, 4, 0.3), (700, 192, "none", False, 2, 0.9), (257, 200, "relu", False, 40, 0.2),
+    (1000, 320, "silu", True, 3, 1.0), (64, 96, "none", False, 300, 0.0),
+])
+def test_epilogue_backward_leaves_nothing_unwritten(M, N, act, gated, E, drop, dtype):
+    """By expert: rows of dropped pairs and the columns past the last segment
+    are zero, in buffers that held something else, also where ld_qt leaves no
+    column past it."""
+    torch_cuda()
+    g = torch.Generator().manual_seed(M + N)
+    ids = mc.ids_of(g, M, 1, E, drop)
+    sort = pkg.sort_tokens(ids.cuda(), E)
+    offsets, k_offsets = mc.order(ids, E)[:2]
+    live, used = offsets[-1], k_offsets[-1]
+    plain = act == "none" and not gated
+    z = None if plain else torch.randn(M, N, generator=g).bfloat16().cuda()
+    d = torch.randn(M, N // 2 if gated else N, generator=g).to(dtype).cuda()
+    wide = (-(-M // 128) + E) * 128
+    say(f"epilogue backward M={M} N={N} act={act} gated={gated} E={E} live={live} used={used} {dtype}")
+    (q0, s0), (qt0, st0), _ = pkg.epilogue_backward(d, z, act=act, gated=gated, sort=sort, bias=False)
+    assert qt0.shape == (N, wide)
+    assert not q0[live:].any() and not s0[live:].any() and not qt0[:, used:].any() and not st0[:, used // 32:].any()
+    for ld_qt in sorted({used, used + 128, wide}):
+        q, s, qt, st = _grad_abi(d, z, act, gated, sort, "e4m3", ld_qt)
+        assert torch.equal(q, q0) and torch.equal(s, s0)
+        assert torch.equal(qt[:, :used], qt0[:, :used]) and torch.equal(st[:, :used // 32], st0[:, :used // 32])
+        assert not qt[:, used:].any() and not st[:, used // 32:].any()
+    q, s, _, _ = _grad_abi(d, z, act, gated, sort, "e4m3", wide, cols=False)
+    assert torch.equal(q, q0) and torch.equal(s, s0)
+    _, _, qt, st = _grad_abi(d, z, act, gated, sort, "e4m3", wide, rows=False)
+    assert torch.equal(qt, qt0) and torch.equal(st, st0)
+
+
+def test_quantize_transposed_leaves_nothing_unwritten():
+    torch_cuda()
+    g = torch.Generator().manual_seed(4)
+    ids = mc.ids_of(g, 300, 2, 6, 0.2)
+    sort = pkg.sort_tokens(ids.cuda(), 6)
+    used = mc.order(ids, 6)[1][-1]
+    x = torch.randn(600, 80, generator=g).bfloat16().cuda()
+    junk = [torch.full((80, 1408), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    del junk        # what an allocation of this size holds next
+    qt, st = pkg.quantize_transposed(x, sort)
+    assert qt.shape == (80, 1408) and not qt[:, used:].any() and not st[:, used // 32:].any()
