@@ -130,9 +130,9 @@ enum { MXGEMM_GROUP_NONE = 0,   /* one product                                  
  *       clamped to the rows (or K) there are
  * K % 128 == 0 (one MFMA K-step), as everywhere in this library.  GROUP_INNER
  * takes no bias, activation, gate, residual or z.
- * Errors: EINVAL, EUNSUPPORTED (K not a multiple of 128; more than 2^31 work
- * items; gated weights, or their scales, that span 4 GiB or more per expert),
- * EHIP.
+ * Errors: EINVAL, EUNSUPPORTED (K not a multiple of 128; row strides of a or w
+ * over 8 MiB, of their scales over 4 MiB; a grid of 2^32 threads or more; gated
+ * weights, or their scales, that span 4 GiB or more per expert), EHIP.
  */
 typedef struct mxgemm_linear {
     const void* a;
@@ -188,7 +188,8 @@ int mxgemm_linear(const mxgemm_linear_t* args, void* stream);
  * transposed).  By expert: offsets, k_offsets int32 [experts + 1], ld_qt >=
  * k_offsets[experts] and a multiple of 128; experts = 0 and NULL otherwise.
  * workspace: ld_qt/128 * N floats, needed for d_bias.
- * Errors: EINVAL, EUNSUPPORTED, EHIP.
+ * Errors: EINVAL, EUNSUPPORTED (more than 65534 chunks of 128 tokens in rows or
+ * ld_qt, more than 65535 experts, N above 2^30 - 1024), EHIP.
  */
 int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out, const void* z, int64_t ld_z,
                              int64_t rows, int64_t N, int32_t act, int32_t gated, const int32_t* offsets,
@@ -201,7 +202,7 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
  * stride ld_src, matrix stride src_batch (bytes): codes or scales held with
  * their inner axis strided, laid out for mxgemm_linear.  Any alignment.
  * Errors: EINVAL, EUNSUPPORTED (more than 65535 matrices or tiles of 128
- * rows), EHIP.
+ * rows, more than 2^31 - 128 columns), EHIP.
  */
 int mxgemm_transpose_bytes(const void* src, int64_t ld_src, int64_t src_batch, int64_t rows, int64_t cols,
                            int64_t batch, void* dst, void* stream);

@@ -65,6 +65,7 @@ enum { kSkinnyNarrow, kSkinny2, kSkinny4, kSkinny8, kSkinnyWide };
 
 struct LinTile {
     int tile_m, tile_n;           // tile_n: columns of the product
+    int threads;                  // of a work-group
 };
 
 hipError_t launch_linear(int cfg, bool exact, int fa, int fw, const LinArgs& a, hipStream_t stream);

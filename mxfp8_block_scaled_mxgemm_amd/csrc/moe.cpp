@@ -35,12 +35,13 @@ hipError_t launch_linear(int cfg, bool exact, int fa, int fw, const LinArgs& a, 
 LinTile lin_tile(int cfg, const LinArgs& a)
 {
     const int few = a.skinny == kSkinnyWide ? 64 : a.skinny == kSkinnyNarrow ? 16 : 32;
+    const int threads = a.skinny == kSkinnyNarrow ? 1024 : a.skinny == kSkinny8 ? 512 : a.skinny == kSkinny2 ? 128 : 256;
     switch (cfg) {
-    case kLin256x256: return {256, 256};
-    case kLin128x128: return {128, 128};
-    case kLin64x64: return {64, 64};
-    case kLinRows32: return {32, few};
-    default: return {16, few};
+    case kLin256x256: return {256, 256, 256};
+    case kLin128x128: return {128, 128, 256};
+    case kLin64x64: return {64, 64, 256};
+    case kLinRows32: return {32, few, threads};
+    default: return {16, few, threads};
     }
 }
 
@@ -140,12 +141,13 @@ int token_args(mxg::TokenArgs* a, int32_t type, int64_t tokens, int32_t k, int64
         return fail(MXGEMM_EINVAL, "unknown element type %d", type);
     if (cols < 1)
         return fail(MXGEMM_EINVAL, "cols %lld must be positive", (long long)cols);
-    // one thread per eight elements, 2^31 - 1 work-groups of 256
+    // one thread per eight elements, at most 128 launches of 2^31
     if (cols > (1 << 24) || (cols + 7) / 8 * tokens > (1LL << 38))
         return fail(MXGEMM_EUNSUPPORTED, "%lld tokens of %lld columns are too many", (long long)tokens,
                     (long long)cols);
     memset(a, 0, sizeof(*a));
     a->tokens = tokens;
+    a->all_rows = tokens * k;
     a->k = k;
     a->cols = (int)cols;
     a->live = offsets + experts;
@@ -340,8 +342,10 @@ int plan_linear(mxg::LinArgs* a, int cfg, int cus, int64_t workspace_bytes)
         work = (work + mxg::kNumXcd - 1) / mxg::kNumXcd * mxg::kNumXcd * a->groups;
     else if (a->mode == mxg::kByRows)
         work = (work + mxg::kNumXcd - 1) / mxg::kNumXcd * mxg::kNumXcd;
-    if (work >= (1LL << 31))
-        return fail(MXGEMM_EUNSUPPORTED, "too many work items");
+    // (the runtime would take a larger grid modulo 2^32 threads, without an error)
+    if (work >= (1LL << 32) / t.threads)
+        return fail(MXGEMM_EUNSUPPORTED, "%lld work-groups of %d threads are too many for one launch", (long long)work,
+                    t.threads);
     a->tiles_m = (int)tiles_m;
     a->tiles_n = (int)tiles_n;
     a->total_work = (int)work;
@@ -568,8 +572,9 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
     if (rows < 0 || N < 1 || experts < 0)
         return fail(MXGEMM_EINVAL, "rows %lld and experts %d must not be negative, N %lld must be positive",
                     (long long)rows, experts, (long long)N);
-    if (rows > (1LL << 31) - 1024 || N > (1LL << 31) - 1024)
-        return fail(MXGEMM_EUNSUPPORTED, "problem too large for 32-bit indexes");
+    // 65534 chunks of 128 tokens; four threads per column of N, below 2^32
+    if (rows > 65534LL * 128 || N > (1LL << 30) - 1024)
+        return fail(MXGEMM_EUNSUPPORTED, "%lld rows or N %lld are too many", (long long)rows, (long long)N);
     if (d_type < MXGEMM_TYPE_BF16 || d_type > MXGEMM_TYPE_FP32)
         return fail(MXGEMM_EINVAL, "unknown element type %d", d_type);
     if (act < MXGEMM_ACT_NONE || act > MXGEMM_ACT_SILU)
@@ -647,7 +652,7 @@ int mxgemm_transpose_bytes(const void* src, int64_t ld_src, int64_t src_batch, i
     if (rows < 0 || cols < 0 || batch < 0)
         return fail(MXGEMM_EINVAL, "sizes must not be negative");
     TRY(check_stride("src", ld_src, cols));
-    if (batch > 65535 || rows > 65535LL * 128 || cols > (1LL << 31))
+    if (batch > 65535 || rows > 65535LL * 128 || cols > (1LL << 31) - 128)
         return fail(MXGEMM_EUNSUPPORTED, "%lld matrices of %lld x %lld bytes are too many", (long long)batch,
                     (long long)rows, (long long)cols);
     if (rows == 0 || cols == 0 || batch == 0)

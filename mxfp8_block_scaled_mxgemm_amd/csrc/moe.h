@@ -34,6 +34,7 @@ struct TokenArgs {
     const int32_t* live;
     const int32_t* row_of;        // [tokens][k]
     int64_t tokens;
+    int64_t all_rows;             // tokens k of the call; a launch may hold fewer tokens
     int k, cols;
     const void* x;                // dispatch: tokens; combine: residual (may be null); backward: d_out
     int64_t ld_x;

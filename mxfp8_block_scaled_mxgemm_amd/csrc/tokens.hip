@@ -236,42 +236,34 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t stream)
 // Kept rows, within the rows there are.
 __device__ __forceinline__ int live_rows(const TokenArgs& p)
 {
-    const int64_t rows = p.tokens * p.k;
     const int live = *p.live;
-    return live < 0 ? 0 : live < rows ? live : (int)rows;
+    return live < 0 ? 0 : live < p.all_rows ? live : (int)p.all_rows;
 }
 
-// Token and piece of flat index i (pieces per token); 32-bit division where
-// the count allows it.
-__device__ __forceinline__ void split_index(int64_t i, int64_t total, int pieces, int64_t& t, int& c)
+// Token and piece of the thread (pieces per token); false past the last.
+// Launches hold at most 2^31 threads.
+__device__ __forceinline__ bool thread_piece(const TokenArgs& p, int pieces, int64_t& t, int& c)
 {
-    if (total <= 0xFFFFFFFFLL) {
-        const uint32_t q = (uint32_t)i / (uint32_t)pieces;
-        t = q;
-        c = (int)((uint32_t)i - q * (uint32_t)pieces);
-    } else {
-        t = i / pieces;
-        c = (int)(i - t * pieces);
-    }
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, q = i / (uint32_t)pieces;
+    t = q;
+    c = (int)(i - q * (uint32_t)pieces);
+    return t < p.tokens;
 }
 
 template <int TYPE, int V>
 __global__ void __launch_bounds__(256) dispatch_kernel(TokenArgs p, int pieces)
 {
     typedef typename Element<TYPE>::T T;
-    const int64_t total = p.tokens * pieces;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total)
-        return;
     int64_t t;
     int piece;
-    split_index(i, total, pieces, t, piece);
+    if (!thread_piece(p, pieces, t, piece))
+        return;
     const int c = piece_start<V>(piece, p.cols);
     Pack<TYPE, V> v, none;
     v.load(static_cast<const T*>(p.x) + t * p.ld_x + c);
     none.zero();
     const int live = live_rows(p);
-    const uint32_t rows = (uint32_t)(p.tokens * p.k);
+    const uint32_t rows = (uint32_t)p.all_rows;
     T* out = static_cast<T*>(p.out) + c;
 #pragma unroll 4
     for (int j = 0; j < p.k; ++j) {
@@ -292,13 +284,10 @@ template <int TYPE, int F>
 __global__ void __launch_bounds__(256) dispatch_mx_kernel(TokenArgs p, int pieces)
 {
     typedef typename Element<TYPE>::T T;
-    const int64_t total = p.tokens * pieces;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total)     // pieces is even: both threads of a block leave together
-        return;
     int64_t t;
     int piece;
-    split_index(i, total, pieces, t, piece);
+    if (!thread_piece(p, pieces, t, piece))     // pieces is even: both threads of a block leave together
+        return;
     const int c = piece * 16;
     Pack<TYPE, 16> v;
     v.load(static_cast<const T*>(p.x) + t * p.ld_x + c);
@@ -316,7 +305,7 @@ __global__ void __launch_bounds__(256) dispatch_mx_kernel(TokenArgs p, int piece
     for (int w = 0; w < 4; ++w)
         code[w] = mx_codes<F>(sc, f[4 * w], f[4 * w + 1], f[4 * w + 2], f[4 * w + 3]);
     const int live = live_rows(p);
-    const uint32_t rows = (uint32_t)(p.tokens * p.k);
+    const uint32_t rows = (uint32_t)p.all_rows;
     uint8_t* q = p.q + c;
     uint8_t* s = p.s + (c >> 5);
 #pragma unroll 4
@@ -343,13 +332,10 @@ template <int TYPE, int V>
 __global__ void __launch_bounds__(256) combine_kernel(TokenArgs p, int pieces)
 {
     typedef typename Element<TYPE>::T T;
-    const int64_t total = p.tokens * pieces;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total)
-        return;
     int64_t t;
     int piece;
-    split_index(i, total, pieces, t, piece);
+    if (!thread_piece(p, pieces, t, piece))
+        return;
     const int c = piece_start<V>(piece, p.cols);
     const int live = live_rows(p);
     const T* rows = static_cast<const T*>(p.rows) + c;
@@ -409,7 +395,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(TokenArgs p, int 
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int live = live_rows(p);
-    const uint32_t nrows = (uint32_t)(p.tokens * p.k);
+    const uint32_t nrows = (uint32_t)p.all_rows;
     const T* d = static_cast<const T*>(p.x) + t * p.ld_x;
     for (int j0 = 0; j0 < p.k; j0 += 8) {
         int r[8];
@@ -468,52 +454,81 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(TokenArgs p, int 
 
 // ---------------------------------------------------------------- launch --
 
-static unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
+// launch(p, work-groups) for ranges of tokens with at most 2^31 threads each,
+// `per_token` threads a token in work-groups of `group`: the runtime takes a
+// grid of 2^32 threads or more modulo 2^32, without an error.  x, d_weights
+// and the k-wide arrays are tokens' own; out is where `out_by_token`.
+template <class Launch>
+static hipError_t by_ranges(const TokenArgs& a, int element, bool out_by_token, int per_token, int group,
+                            const Launch& launch)
+{
+    const int64_t most = (1LL << 31) / per_token;
+    for (int64_t t = 0; t < a.tokens; t += most) {
+        TokenArgs p = a;
+        p.tokens = a.tokens - t < most ? a.tokens - t : most;
+        p.row_of += t * a.k;
+        p.x = a.x ? static_cast<const char*>(a.x) + t * a.ld_x * element : nullptr;
+        p.weights = a.weights ? a.weights + t * a.k : nullptr;
+        p.d_weights = a.d_weights ? a.d_weights + t * a.k : nullptr;
+        if (out_by_token)
+            p.out = static_cast<char*>(a.out) + t * a.ld_out * element;
+        launch(p, (unsigned)((p.tokens * per_token + group - 1) / group));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+// Threads of 256 per token for pieces of V elements, and the launch of a
+// kernel that takes them so.
+#define MXG_LAUNCH_PIECES(kernel, V, element, out_by_token)                                               \
+    do {                                                                                                  \
+        const int pieces = (a.cols + V - 1) / V;                                                          \
+        return by_ranges(a, element, out_by_token, pieces, 256, [&](const TokenArgs& p, unsigned groups) { \
+            hipLaunchKernelGGL(kernel, dim3(groups), dim3(256), 0, stream, p, pieces);                    \
+        });                                                                                               \
+    } while (0)
 
 template <int TYPE>
 static hipError_t dispatch_type(const TokenArgs& a, hipStream_t stream)
 {
-    if (a.cols >= 8) {
-        const int pieces = (a.cols + 7) / 8;
-        hipLaunchKernelGGL((dispatch_kernel<TYPE, 8>), dim3(blocks_of(a.tokens * pieces)), dim3(256), 0, stream, a, pieces);
-    } else {
-        hipLaunchKernelGGL((dispatch_kernel<TYPE, 1>), dim3(blocks_of(a.tokens * a.cols)), dim3(256), 0, stream, a, a.cols);
-    }
-    return hipGetLastError();
+    constexpr int element = sizeof(typename Element<TYPE>::T);
+    if (a.cols >= 8)
+        MXG_LAUNCH_PIECES((dispatch_kernel<TYPE, 8>), 8, element, false);
+    MXG_LAUNCH_PIECES((dispatch_kernel<TYPE, 1>), 1, element, false);
 }
 
 template <int TYPE>
 static hipError_t dispatch_mx_type(const TokenArgs& a, hipStream_t stream)
 {
-    const int pieces = a.cols / 16;
-    const dim3 grid(blocks_of(a.tokens * pieces));
+    constexpr int element = sizeof(typename Element<TYPE>::T);
     if (a.fmt == kE5M2)
-        hipLaunchKernelGGL((dispatch_mx_kernel<TYPE, kE5M2>), grid, dim3(256), 0, stream, a, pieces);
-    else
-        hipLaunchKernelGGL((dispatch_mx_kernel<TYPE, kE4M3>), grid, dim3(256), 0, stream, a, pieces);
-    return hipGetLastError();
+        MXG_LAUNCH_PIECES((dispatch_mx_kernel<TYPE, kE5M2>), 16, element, false);
+    MXG_LAUNCH_PIECES((dispatch_mx_kernel<TYPE, kE4M3>), 16, element, false);
 }
 
 template <int TYPE>
 static hipError_t combine_type(const TokenArgs& a, hipStream_t stream)
 {
-    if (a.cols >= 8) {
-        const int pieces = (a.cols + 7) / 8;
-        hipLaunchKernelGGL((combine_kernel<TYPE, 8>), dim3(blocks_of(a.tokens * pieces)), dim3(256), 0, stream, a, pieces);
-    } else {
-        hipLaunchKernelGGL((combine_kernel<TYPE, 1>), dim3(blocks_of(a.tokens * a.cols)), dim3(256), 0, stream, a, a.cols);
-    }
-    return hipGetLastError();
+    constexpr int element = sizeof(typename Element<TYPE>::T);
+    if (a.cols >= 8)
+        MXG_LAUNCH_PIECES((combine_kernel<TYPE, 8>), 8, element, true);
+    MXG_LAUNCH_PIECES((combine_kernel<TYPE, 1>), 1, element, true);
 }
 
 template <int TYPE>
 static hipError_t combine_backward_type(const TokenArgs& a, hipStream_t stream)
 {
+    constexpr int element = sizeof(typename Element<TYPE>::T);
     if (a.cols >= 8)
-        hipLaunchKernelGGL((combine_backward_kernel<TYPE, 8>), dim3((unsigned)a.tokens), dim3(256), 0, stream, a, (a.cols + 7) / 8);
-    else
-        hipLaunchKernelGGL((combine_backward_kernel<TYPE, 1>), dim3((unsigned)a.tokens), dim3(64), 0, stream, a, a.cols);
-    return hipGetLastError();
+        return by_ranges(a, element, false, 256, 256, [&](const TokenArgs& p, unsigned groups) {
+            hipLaunchKernelGGL((combine_backward_kernel<TYPE, 8>), dim3(groups), dim3(256), 0, stream, p,
+                               (a.cols + 7) / 8);
+        });
+    return by_ranges(a, element, false, 64, 64, [&](const TokenArgs& p, unsigned groups) {
+        hipLaunchKernelGGL((combine_backward_kernel<TYPE, 1>), dim3(groups), dim3(64), 0, stream, p, a.cols);
+    });
 }
 
 #define MXG_BY_TYPE(name)                                                       \

@@ -7,7 +7,7 @@ import torch
 import mxfp8_block_scaled_mxgemm_amd as pkg
 import moe_common as mc
 from gpu_common import say, torch_cuda
-from mxfp8_block_scaled_mxgemm_amd import _moe
+from mxfp8_block_scaled_mxgemm_amd import _lib, _moe
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,83 @@ def test_quantize_transposed_leaves_nothing_unwritten():
     del junk        # what an allocation of this size holds next
     qt, st = pkg.quantize_transposed(x, sort)
     assert qt.shape == (80, 1408) and not qt[:, used:].any() and not st[:, used // 32:].any()
+
+
+def test_combine_backward_of_many_tokens():
+    """More tokens than one launch takes with a work-group of 256 threads each."""
+    torch_cuda()
+    T, H = (1 << 24) + 3, 8
+    pair = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    live = T - 5
+    sort = pkg.TokenSort(torch.tensor([0, live], dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                         pair.view(T, 1), pair)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    whole = lambda *s: torch.randint(-4, 5, s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    rows, d, w = whole(T, H), whole(T, H), whole(T, 1).float()
+    say(f"combine backward T={T}")
+    d_rows, d_w = pkg.combine_tokens_backward(d, rows, sort, w)
+    ref = (w * d.float()).bfloat16().flip(0)
+    ref[live:] = 0
+    assert torch.equal(d_rows, ref)
+    rows = rows.flip(0)                     # token t's row
+    rows[:T - live] = 0
+    assert torch.equal(d_w, (rows.float() * d.float()).sum(1, keepdim=True))
+    out = pkg.combine_tokens(d_rows, sort, w)
+    assert torch.equal(out, (w * d_rows.flip(0).float()).bfloat16().masked_fill(
+        (torch.arange(T, device="cuda") < T - live).unsqueeze(1), 0))
+
+
+def test_more_pieces_than_one_launch():
+    """Seven columns, a thread per element: over 2^32 threads."""
+    torch_cuda()
+    T, H = 614_000_001, 7
+    assert T * H > 1 << 32
+    pair = torch.arange(T, dtype=torch.int32, device="cuda")
+    sort = pkg.TokenSort(torch.tensor([0, T - 1], dtype=torch.int32, device="cuda"),
+                         torch.zeros(2, dtype=torch.int32, device="cuda"), pair.view(T, 1), pair)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    step = 1 << 27
+    for i in range(0, T, step):
+        x[i:i + step] = torch.randint(-9, 10, (min(step, T - i), H), device="cuda", dtype=torch.int8)
+    say(f"dispatch and combine T={T} H={H}")
+    rows = pkg.dispatch_tokens(x, sort)
+    x[T - 1] = 0            # the last token's pair is dropped
+    assert all(torch.equal(rows[i:i + step], x[i:i + step]) for i in range(0, T, step))
+    x.zero_()
+    out = pkg.combine_tokens(rows, sort, residual=x)
+    assert all(torch.equal(rows[i:i + step], out[i:i + step]) for i in range(0, T, step))
+
+
+def test_mx_dispatch_over_two_launches():
+    """Token ranges of a launch begin at the right rows of x and row_of."""
+    torch_cuda()
+    T, H = (1 << 30) + 7, 32        # two threads a token: just over 2^31
+    pair = torch.arange(T, dtype=torch.int32, device="cuda")
+    sort = pkg.TokenSort(torch.tensor([0, T - 3], dtype=torch.int32, device="cuda"),
+                         torch.zeros(2, dtype=torch.int32, device="cuda"), pair.view(T, 1), pair)
+    x = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    x[1 << 30:] = 3.0
+    say(f"dispatch mx T={T} H={H}")
+    q, s = pkg.dispatch_tokens_mx(x, sort)
+    del x
+    small = torch.tensor([[1.0] * H, [3.0] * H], device="cuda")
+    rq, rs = pkg.quantize_mxfp8(small)
+    step = 1 << 27
+    for i in range(0, T, step):
+        lo, hi = i, min(i + step, T)
+        which = (pair[lo:hi] >= 1 << 30).long()
+        kept = (pair[lo:hi] < T - 3).unsqueeze(1)
+        assert torch.equal(s[lo:hi], rs[which] * kept) and torch.equal(q[lo:hi], rq[which] * kept)
+
+
+def test_product_of_too_many_work_groups_is_refused():
+    """2^26 tiles of 64 x 64 with 256 threads each: the host refuses, nothing is
+    launched."""
+    torch_cuda()
+    n = 1 << 19
+    p = torch.zeros(4096, dtype=torch.uint8, device="cuda").data_ptr()
+    say("refusal of a grid of 2^34 threads")
+    rc = _moe._load().mxgemm_linear(_moe.LINEAR_ARGS.pack(
+        p, p, p, p, 0, 0, p, 0, 0, 0, n, n, 128, 128, 4, 128, 4, 0, 0, 0, n, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 2, 0, 0),
+        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == _lib.MXGEMM_EUNSUPPORTED, (rc, pkg.last_error())

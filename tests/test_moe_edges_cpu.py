@@ -1,0 +1,19 @@
+"""CPU-only checks of edges of the expert layer's host side."""
+import ctypes
+
+from mxfp8_block_scaled_mxgemm_amd import _lib, _moe
+
+
+def test_grids_of_2_to_32_threads_are_refused():
+    """What one launch cannot hold is EUNSUPPORTED before anything else is
+    looked at."""
+    lib = _moe._load()
+    p = ctypes.c_void_p(16)
+    eb = lib.mxgemm_epilogue_backward
+    N = 1 << 30
+    assert eb(p, 0, N, None, 0, 4, N, 0, 0, None, None, 0, 0, p, p, p, p, 128, None, None, 0,
+              None) == _lib.MXGEMM_EUNSUPPORTED
+    rows = 65535 * 128
+    assert eb(p, 0, 64, None, 0, rows, 64, 0, 0, p, p, 2, 0, p, p, p, p, 128, None, None, 0,
+              None) == _lib.MXGEMM_EUNSUPPORTED
+    assert lib.mxgemm_transpose_bytes(p, 1 << 31, 0, 4, 1 << 31, 1, p, None) == _lib.MXGEMM_EUNSUPPORTED
