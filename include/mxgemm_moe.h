@@ -185,8 +185,9 @@ int mxgemm_linear(const mxgemm_linear_t* args, void* stream);
  * Any of (q, s), (qt, st) and d_bias may be NULL.  d_out [rows][cols] of
  * d_type; z bfloat16 [rows][N], NULL only for act NONE and not gated (then
  * this quantises d_out itself, both ways, which is how a and w are laid out
- * transposed).  By expert: offsets, k_offsets int32 [experts + 1], ld_qt >=
- * k_offsets[experts] and a multiple of 128; experts = 0 and NULL otherwise.
+ * transposed) or for no rows.  By expert: offsets, k_offsets int32
+ * [experts + 1], ld_qt >= k_offsets[experts] and a multiple of 128; experts = 0
+ * and NULL otherwise.
  * workspace: ld_qt/128 * N floats, needed for d_bias.
  * Errors: EINVAL, EUNSUPPORTED (more than 65534 chunks of 128 tokens in rows or
  * ld_qt, more than 65535 experts, N above 2^30 - 1024), EHIP.

@@ -408,6 +408,8 @@ def _epilogue_backward(d_out, z, act, gated, sort, fmt, rows, cols, bias):
     ld_d = _rows_of(d_out, "d_out", dtypes=_TYPES)
     M = d_out.shape[0]
     N = d_out.shape[1] * (2 if gated else 1)
+    if z is None and (gated or _activation(act)):
+        raise ValueError("an activation's gradient needs z")
     ld_z = 0 if z is None else _rows_of(z, "z", dev, (torch.bfloat16,), (M, N))
     E = off = koff = 0
     ld_qt = _up(M, STEP)

@@ -583,7 +583,7 @@ int mxgemm_epilogue_backward(const void* d_out, int32_t d_type, int64_t ld_d_out
         return fail(MXGEMM_EINVAL, "unknown FP8 format %d", format);
     if (gated && N % 2 != 0)
         return fail(MXGEMM_EINVAL, "a gated product needs an even N, not %lld", (long long)N);
-    if (!z && (gated || act != MXGEMM_ACT_NONE))
+    if (rows > 0 && !z && (gated || act != MXGEMM_ACT_NONE))     // an array of no rows may be NULL
         return fail(MXGEMM_EINVAL, "an activation's gradient needs z");
     if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st == nullptr))
         return fail(MXGEMM_EINVAL, "codes and scales come together (q with s, qt with st)");

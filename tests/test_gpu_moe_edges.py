@@ -1,5 +1,7 @@
 """Edges of the expert layer on the GPU."""
 import ctypes
+import importlib.util
+import os
 
 import pytest
 import torch
@@ -10,6 +12,7 @@ from gpu_common import say, torch_cuda
 from mxfp8_block_scaled_mxgemm_amd import _lib, _moe
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _filled(*shape):
@@ -161,3 +164,42 @@ def test_product_of_too_many_work_groups_is_refused():
         p, p, p, p, 0, 0, p, 0, 0, 0, n, n, 128, 128, 4, 128, 4, 0, 0, 0, n, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 2, 0, 0),
         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
     assert rc == _lib.MXGEMM_EUNSUPPORTED, (rc, pkg.last_error())
+
+
+@pytest.mark.parametrize("by", [False, True])
+@pytest.mark.parametrize("act,gated", [("silu", False), ("gelu", False), ("silu", True), ("none", True),
+                                       ("gelu_tanh", True), ("relu", False)])
+def test_no_tokens_behind_an_activation(act, gated, by):
+    torch_cuda()
+    N, K, E = 64, 128, 3
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    sort = pkg.sort_tokens(torch.empty(0, 2, dtype=torch.int32, device="cuda"), E) if by else None
+    lead, Mp = ((E,), E * 128) if by else ((), 0)
+    d = torch.empty(0, N // 2 if gated else N, dtype=torch.bfloat16, device="cuda")
+    z = torch.empty(0, N, dtype=torch.bfloat16, device="cuda")
+    got = pkg.linear_backward(d, z, torch.zeros(K, Mp, **u8), torch.zeros(K, Mp // 32, **u8),
+                              torch.zeros(*lead, K, 128, **u8), torch.zeros(*lead, K, 4, **u8), act=act, gated=gated,
+                              sort=sort)
+    assert got.d_a.shape == (0, K) and got.d_w.shape == (*lead, N, K) and got.d_bias.shape == (*lead, N)
+    assert not got.d_w.any() and not got.d_bias.any()
+    with pytest.raises(ValueError):
+        pkg.epilogue_backward(d, None, act=act, gated=gated, sort=sort)
+
+
+def test_layer_without_tokens():
+    """A rank that receives no token: serving and training steps of the whole
+    layer."""
+    torch_cuda()
+    spec = importlib.util.spec_from_file_location("moe_layer", os.path.join(ROOT, "examples", "moe_layer.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    E, H, F = 3, 256, 128
+    w1, w2 = torch.randn(E, 2 * F, H, device="cuda").bfloat16(), torch.randn(E, H, F, device="cuda").bfloat16()
+    layer = example.ExpertLayer(w1, w2)
+    x = torch.empty(0, H, dtype=torch.bfloat16, device="cuda")
+    ids, weights = torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda")
+    say("layer T=0")
+    assert layer.forward(x, ids, weights).shape == (0, H)
+    y, (d_x, d_weights, d_w1, d_w2) = layer.train_step(x, ids, weights, x)
+    assert y.shape == d_x.shape == (0, H) and d_weights.shape == (0, 2)
+    assert d_w1.shape == w1.shape and d_w2.shape == w2.shape and not d_w1.any() and not d_w2.any()

@@ -1,6 +1,7 @@
 """CPU-only checks of edges of the expert layer's host side."""
 import ctypes
 
+import mxfp8_block_scaled_mxgemm_amd as pkg
 from mxfp8_block_scaled_mxgemm_amd import _lib, _moe
 
 
@@ -17,3 +18,12 @@ def test_grids_of_2_to_32_threads_are_refused():
     assert eb(p, 0, 64, None, 0, rows, 64, 0, 0, p, p, 2, 0, p, p, p, p, 128, None, None, 0,
               None) == _lib.MXGEMM_EUNSUPPORTED
     assert lib.mxgemm_transpose_bytes(p, 1 << 31, 0, 4, 1 << 31, 1, p, None) == _lib.MXGEMM_EUNSUPPORTED
+
+
+def test_no_rows_need_no_preactivation():
+    """A NULL z is refused for real rows only."""
+    eb = _moe._load().mxgemm_epilogue_backward
+    args = lambda rows, ld: (None, 0, 64, None, 64, rows, 64, 4, 0, None, None, 0, 0, None, None, None, None,  # noqa: E731
+                             ld, None, None, 0, None)
+    assert eb(*args(4, 128)) == _lib.MXGEMM_EINVAL and "needs z" in pkg.last_error()
+    assert eb(*args(0, 0)) != _lib.MXGEMM_EINVAL        # without a GPU the call ends at the device
