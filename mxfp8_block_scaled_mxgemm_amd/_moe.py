@@ -406,6 +406,8 @@ def _epilogue_backward(d_out, z, act, gated, sort, fmt, rows, cols, bias):
     asked for."""
     dev = d_out.device
     ld_d = _rows_of(d_out, "d_out", dtypes=_TYPES)
+    if d_out.dim() != 2:
+        raise ValueError(f"expected a matrix [rows, columns], got {tuple(d_out.shape)}")
     M = d_out.shape[0]
     N = d_out.shape[1] * (2 if gated else 1)
     if z is None and (gated or _activation(act)):

@@ -203,3 +203,13 @@ def test_layer_without_tokens():
     y, (d_x, d_weights, d_w1, d_w2) = layer.train_step(x, ids, weights, x)
     assert y.shape == d_x.shape == (0, H) and d_weights.shape == (0, 2)
     assert d_w1.shape == w1.shape and d_w2.shape == w2.shape and not d_w1.any() and not d_w2.any()
+
+
+def test_gradient_takes_matrices_only():
+    """A stack of matrices is refused, not read as one of its corners."""
+    torch_cuda()
+    x = torch.randn(3, 64, 128, device="cuda").bfloat16()
+    for bad in (lambda: pkg.quantize_transposed(x), lambda: pkg.epilogue_backward(x),
+                lambda: pkg.epilogue_backward(x, x, act="silu"), lambda: pkg.quantize_transposed(x[None])):
+        with pytest.raises(ValueError):
+            bad()
