@@ -34,7 +34,9 @@ enum { MXGEMM_TYPE_BF16 = 0, MXGEMM_TYPE_FP16 = 1, MXGEMM_TYPE_FP32 = 2, MXGEMM_
        MXGEMM_TYPE_MXE5M2 = 4 };
 
 /* Activations, computed in FP32: max(z, 0); 0.5 z (1 + erf(z / sqrt 2));
- * 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); z / (1 + exp(-z)). */
+ * 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); z / (1 + exp(-z)).  Exponentials
+ * and reciprocals are the hardware's (a unit in the last place; an exponential
+ * also carries the rounding of its argument). */
 enum { MXGEMM_ACT_NONE = 0, MXGEMM_ACT_RELU = 1, MXGEMM_ACT_GELU = 2, MXGEMM_ACT_GELU_TANH = 3,
        MXGEMM_ACT_SILU = 4 };
 

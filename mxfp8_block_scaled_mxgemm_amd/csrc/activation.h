@@ -15,17 +15,28 @@ constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
 __device__ __forceinline__ float relu(float z) { return z != z ? z : fmaxf(z, 0.f); }
-// The normal distribution function 0.5 (1 + erf(z / sqrt 2)), erf by
-// Abramowitz and Stegun's formula 7.1.26 (error below 1.5e-7), without the
-// branches of a full-precision erf: the epilogue is bound by instructions.
-// The tail is formed on the side where it is small, so nothing cancels there.
+// The normal distribution function 0.5 (1 + erf(z / sqrt 2)).  Its tail is
+// exp(-z^2 / 2) times a smooth function of |z|, which is fitted as a polynomial
+// in t = 1 / (1 + 0.35 |z|): least largest relative error over |z| <= 15
+// (3.2e-8; beyond, the tail is below FP32's range), by iteratively reweighted
+// least squares.  No branches, as a full-precision erf has: the epilogue is
+// bound by instructions.  The tail is formed on the side where it is small, so
+// nothing cancels there.  Evaluated in FP32: 1.8e-8 off in rms over gelu of
+// N(0, 1), and by 7e-7 of the value at z = -3, 7e-6 at -12 (the rounding of
+// z^2 / 2).  Four steps fewer, good to 1.5e-7 absolute, save 0.6% of 8192 x
+// 8192 x 8192 native with gelu and 3% of x 2048.
 __device__ __forceinline__ float normal_cdf(float z)
 {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
-    const float poly =
-        t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * poly * __expf(-x * x);
+    const float t = __builtin_amdgcn_rcpf(1.f + 0.35f * fabsf(z));
+    float p = 0.144060203f - 0.0291637983f * t;
+    p = -0.255900672f + t * p;
+    p = 0.159391613f + t * p;
+    p = -0.0232629887f + t * p;
+    p = 0.105574466f + t * p;
+    p = 0.119815577f + t * p;
+    p = 0.139864326f + t * p;
+    p = 0.139621259f + t * p;
+    const float tail = t * p * __expf(-0.5f * z * z);
     return z < 0.f ? tail : 1.f - tail;
 }
 __device__ __forceinline__ float gelu(float z) { return z * normal_cdf(z); }

@@ -213,3 +213,35 @@ def test_gradient_takes_matrices_only():
                 lambda: pkg.epilogue_backward(x, x, act="silu"), lambda: pkg.quantize_transposed(x[None])):
         with pytest.raises(ValueError):
             bad()
+
+
+# -------------------------------------------------------------------- gelu --
+
+def test_gelu_keeps_float32_in_its_tail():
+    """gelu and its slope against 64 bits, relative to themselves: with a = z^2
+    / 2, exp(-a) in float32 is good to (a 2.5 + 2) units (a's rounding, that of
+    its product with log2 e, the constant's, the hardware's last place), and
+    the reciprocal, the polynomial's nine steps and the products to less than
+    30 more."""
+    torch_cuda()
+    N = 4096
+    z = torch.cat([torch.linspace(-13, 13, 2 * N - 512), -torch.logspace(-8, 1, 256), torch.logspace(-8, 1, 256)])
+    z = z.bfloat16().float()
+    zero = torch.zeros(1, 128, dtype=torch.uint8).cuda(), torch.full((1, 4), 127, dtype=torch.uint8).cuda()
+    n = z.numel()
+    w = torch.zeros(n, 128, dtype=torch.uint8).cuda(), torch.full((n, 4), 127, dtype=torch.uint8).cuda()
+    zd = z.double()
+    units = (3 * zd * zd / 2 + 32) * 2.0 ** -24
+    cdf = 0.5 * torch.special.erfc(-zd / 2 ** 0.5)
+    pdf = torch.exp(-zd * zd / 2) / (2 * torch.pi) ** 0.5
+    out = pkg.linear(*zero, *w, bias=z.cuda(), act="gelu", out_dtype=torch.float32).cpu().double()[0]
+    # at z > 0 the tail is taken from one
+    tail = torch.minimum(cdf, 1 - cdf)
+    bound = zd.abs() * (units * tail + (zd > 0) * 2.0 ** -23) + 2.0 ** -126
+    mc.assert_within(out, zd * cdf, bound, "gelu")
+    for pad in (0, 1):      # whole eights, and not
+        d = torch.ones(1, n + pad)
+        fz = torch.nn.functional.pad(z, (0, pad)).view(1, -1)
+        _, _, db = pkg.epilogue_backward(d.bfloat16().cuda(), fz.bfloat16().cuda(), act="gelu")
+        bound = units * (tail + zd.abs() * pdf) + (zd > 0) * 2.0 ** -23 + 2.0 ** -23 * (cdf + zd * pdf).abs() + 2.0 ** -126
+        mc.assert_within(db[:n], cdf + zd * pdf, bound, "slope")
