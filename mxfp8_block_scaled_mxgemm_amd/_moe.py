@@ -90,9 +90,12 @@ _TYPES = {}
 
 
 def _bind():
+    """Fills the table of types, then binds torch: a thread that finds it bound
+    finds the table filled."""
     global torch
-    import torch
-    _TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    import torch as module
+    _TYPES.update({module.bfloat16: 0, module.float16: 1, module.float32: 2})
+    torch = module
 
 
 def _on_stream(fn):

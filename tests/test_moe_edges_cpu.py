@@ -1,6 +1,8 @@
 """CPU-only checks of edges of the expert layer's host side."""
 import ctypes
 
+import pytest
+
 import mxfp8_block_scaled_mxgemm_amd as pkg
 from mxfp8_block_scaled_mxgemm_amd import _lib, _moe
 
@@ -27,3 +29,22 @@ def test_no_rows_need_no_preactivation():
                              ld, None, None, 0, None)
     assert eb(*args(4, 128)) == _lib.MXGEMM_EINVAL and "needs z" in pkg.last_error()
     assert eb(*args(0, 0)) != _lib.MXGEMM_EINVAL        # without a GPU the call ends at the device
+
+
+def test_first_call_from_two_threads():
+    """torch counts as bound only once the table of types is filled."""
+    torch = pytest.importorskip("torch")
+
+    class Watched(dict):
+        def update(self, *a, **kw):
+            seen.append(_moe.torch)
+            super().update(*a, **kw)
+
+    seen, before = [], (_moe.torch, _moe._TYPES)
+    _moe.torch, _moe._TYPES = None, Watched()
+    try:
+        _moe._bind()
+        assert seen and all(t is None for t in seen)
+        assert _moe.torch is torch and len(_moe._TYPES) == 3
+    finally:
+        _moe.torch, _moe._TYPES = before
