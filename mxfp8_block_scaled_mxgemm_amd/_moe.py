@@ -308,6 +308,11 @@ def _laid_out(t):
     return out
 
 
+def _split_workspace(M, N, K):
+    """mxgemm_linear_workspace's rule, without a call into the library."""
+    return 4 << 20 if M > 32 and K >= 2048 and -(-M // 64) * -(-N // 64) <= 128 else 0
+
+
 def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, out_dtype, preact, precision, a_fmt,
             w_fmt, tile_cfg):
     u8 = (torch.uint8,)
@@ -360,10 +365,9 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
         z = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         z_ptr = z.data_ptr()
         result.append(z)
-    work_ptr = work = 0
-    # mxgemm_linear_workspace's rule
-    if mode == GROUP_NONE and M > 32 and K >= 2048 and -(-M // 64) * -(-N // 64) <= 128:
-        work = 4 << 20
+    work_ptr = 0
+    work = _split_workspace(M, N, K) if mode == GROUP_NONE else 0
+    if work:
         work_mem = torch.empty(work, dtype=torch.uint8, device=dev)
         work_ptr = work_mem.data_ptr()
     w_group, w_scale_group = (w.stride(0), w_scale.stride(0)) if by_row else (0, 0)

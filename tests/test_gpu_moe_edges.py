@@ -215,6 +215,139 @@ def test_gradient_takes_matrices_only():
             bad()
 
 
+def test_stores_past_32_bits():
+    """Outputs whose rows lie more than 2^32 elements apart."""
+    torch_cuda()
+    T, H, K = 3, 64, 128
+    g = torch.Generator().manual_seed(7)
+    ld = (1 << 32) + 64
+    big = torch.zeros(2 * ld + H, dtype=torch.bfloat16, device="cuda")
+    far = torch.as_strided(big, (T, H), (ld, 1))
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    lib = _moe._load()
+    x = torch.randn(T, H, generator=g).bfloat16().cuda()
+    sort = pkg.sort_tokens(torch.tensor([[2], [0], [1]], dtype=torch.int32, device="cuda"), 3)
+    off, row_of = _pointer(sort.offsets), _pointer(sort.row_of)
+    p = _pointer
+    say("dispatch, combine and linear with rows 2^32 + 64 elements apart")
+    assert lib.mxgemm_dispatch_tokens(p(x), H, 0, T, 1, H, off, 3, row_of, p(big), ld, stream) == 0
+    assert torch.equal(far.contiguous(), pkg.dispatch_tokens(x, sort))
+    far.zero_()
+    assert lib.mxgemm_combine_tokens(p(x), H, 0, T, 1, H, off, 3, row_of, None, None, 0, p(big), ld, stream) == 0
+    assert torch.equal(far.contiguous(), pkg.combine_tokens(x, sort))
+    far.zero_()
+    d_w = torch.empty(T, 1, device="cuda")
+    assert lib.mxgemm_combine_tokens_backward(p(x), H, p(x), H, 0, T, 1, H, off, 3, row_of, None, p(big), ld, p(d_w),
+                                              stream) == 0
+    assert torch.equal(far.contiguous(), pkg.combine_tokens_backward(x, x, sort)[0])
+    a, a_s, w, w_s = (t.cuda() for t in (*mc.codes(g, (T, K), "e4m3"), *mc.codes(g, (H, K), "e4m3")))
+    for cfg in (1, 2, 4):
+        ref, z = pkg.linear(a, a_s, w, w_s, act="silu", preact=True, tile_cfg=cfg)
+        out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+        for outp, ldo, zp, ldz, want in ((big, ld, out, H, ref), (out, H, big, ld, z)):
+            far.zero_()
+            rc = lib.mxgemm_linear(_moe.LINEAR_ARGS.pack(
+                a.data_ptr(), a_s.data_ptr(), w.data_ptr(), w_s.data_ptr(), 0, 0, outp.data_ptr(), 0, zp.data_ptr(), 0,
+                T, H, K, K, K // 32, K, K // 32, 0, 0, 0, ldo, 0, 0, ldz, 0, 0, 0, 0, 0, 0, 4, 0, 0, cfg, 0, 0), stream)
+            assert rc == 0, pkg.last_error()
+            assert torch.equal(far.contiguous(), want), cfg
+    del big, far
+
+
+# ---------------------------------------------------------------- products --
+
+TILES = {0: False, 1: True, 2: True, 3: True, 4: True}      # configuration: has it an exact kernel
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("precision", ["exact", "native"])
+@pytest.mark.parametrize("cfg", [-1, *sorted(TILES)])
+def test_linear_by_inner(cfg, precision, out_dtype):
+    """Inner ranges that are empty, a K-step, several and many; columns beyond
+    the last range are no expert's."""
+    torch_cuda()
+    if precision == "exact" and not TILES.get(cfg, True):
+        pytest.skip("no exact kernel of this tile")
+    steps = [0, 1, 3, 0, 6, 17]
+    offsets = [0]
+    for n in steps:
+        offsets.append(offsets[-1] + 128 * n)
+    K = offsets[-1] + 256
+    off = torch.tensor(offsets, dtype=torch.int32).cuda()
+    g = torch.Generator().manual_seed(cfg + 3)
+    for M, N, a_fmt in ((300, 264, "e5m2"), (37, 50, "e4m3")):
+        say(f"by inner M={M} N={N} K={K} cfg={cfg} {precision} {out_dtype} {a_fmt}")
+        a, a_s = mc.codes(g, (M, K), a_fmt)
+        w, w_s = mc.codes(g, (N, K), "e4m3")
+        a[:, offsets[-1]:], a_s[:, offsets[-1] // 32:] = 0x7F, 0xFF         # never read
+        out = pkg.linear_by_inner(a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda(), off, out_dtype=out_dtype,
+                                  precision=precision, a_fmt=a_fmt, tile_cfg=cfg)
+        assert out.shape == (len(steps), M, N) and out.dtype == out_dtype
+        av, wv = mc.value(a, a_s, a_fmt), mc.value(w, w_s, "e4m3")
+        for e in range(len(steps)):
+            u, v = av[:, offsets[e]:offsets[e + 1]], wv[:, offsets[e]:offsets[e + 1]]
+            ref = u @ v.t()
+            t = mc.product_error(u.abs() @ v.abs().t(), u.shape[1], precision)
+            mc.assert_within(out[e], ref, t + mc.rounding(ref.abs() + t, out_dtype), f"expert {e}")
+
+
+def _integers(g, M, N, K, lead=()):
+    """Operands whose products and sums are exact in every step."""
+    one = lambda v: (v.to(torch.float8_e4m3fn).view(torch.uint8),  # noqa: E731
+                     torch.full((*v.shape[:-1], K // 32), 127, dtype=torch.uint8, device="cuda"))
+    av = torch.randint(-1, 2, (M, K), generator=g, device="cuda").float()
+    wv = torch.randint(-2, 3, (*lead, N, K), generator=g, device="cuda").float()
+    wv = torch.where(torch.rand(wv.shape, generator=g, device="cuda") < 0.05, wv, 0.0)
+    return av, wv, one(av), one(wv)
+
+
+@pytest.mark.parametrize("E,N", [(2, 32768), (4, 16384 - 96)])
+def test_large_native_product_by_expert(E, N):
+    """Rows and columns enough for the largest tile by its own rule, ragged."""
+    torch_cuda()
+    K, M = 2048, 1100 * E
+    g = torch.Generator(device="cuda").manual_seed(E)
+    av, wv, (a, a_s), (w, w_s) = _integers(g, M, N, K, (E,))
+    say(f"native by expert M={M} N={N} K={K} E={E}")
+    # unequal shares, some rows dropped
+    offsets = [0] + [1100 * e + 37 * (e % 2) for e in range(1, E)] + [M - 60]
+    out = pkg.linear(a, a_s, w, w_s, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                     out_dtype=torch.float32, precision="native")
+    for e in range(E):
+        lo, hi = offsets[e], offsets[e + 1]
+        assert torch.equal(out[lo:hi], torch.mm(av[lo:hi], wv[e].t())), e
+    assert not out[M - 60:].any()
+
+
+def _codes(g, *shape):
+    """Any finite E4M3 codes under scales of 2^-9 .. 2^0, made on the GPU."""
+    q = torch.randint(0, 256, shape, generator=g, device="cuda", dtype=torch.uint8)
+    return (torch.where((q & 0x7F) == 0x7F, 0, q).to(torch.uint8),
+            torch.randint(118, 128, (*shape[:-1], shape[-1] // 32), generator=g, device="cuda", dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("precision", ["exact", "native"])
+@pytest.mark.parametrize("M,N,K,by", [(4096, 4096, 2176, 0), (3000, 2000, 1152, 0), (64, 2048, 7168, 0),
+                                      (16, 4096, 4096, 0), (3000, 2048, 1024, 12), (9000, 8192, 2048, 8)])
+def test_products_repeat_bit_for_bit(M, N, K, by, precision):
+    """The same inputs give the same bits on every call, with other work in
+    between."""
+    torch_cuda()
+    g = torch.Generator(device="cuda").manual_seed(M)
+    (a, a_s), (w, w_s) = _codes(g, M, K), _codes(g, *((by,) if by else ()), N, K)
+    offsets = None
+    if by:
+        offsets = pkg.sort_tokens(mc.ids_of(torch.Generator().manual_seed(M), M, 1, by, 0.05).cuda(), by).offsets
+    say(f"repeat M={M} N={N} K={K} by={by} {precision}")
+    run = lambda x: pkg.linear(x, a_s, w, w_s, act="silu", offsets=offsets, precision=precision)  # noqa: E731
+    first = run(a)
+    assert not torch.isnan(first).any()
+    other = a.flip(0)
+    for _ in range(6):
+        run(other)
+        assert torch.equal(run(a), first)
+
+
 # -------------------------------------------------------------------- gelu --
 
 def test_gelu_keeps_float32_in_its_tail():

@@ -48,3 +48,12 @@ def test_first_call_from_two_threads():
         assert _moe.torch is torch and len(_moe._TYPES) == 3
     finally:
         _moe.torch, _moe._TYPES = before
+
+
+def test_the_bindings_workspace_rule_is_the_librarys():
+    ws = _moe._load().mxgemm_linear_workspace
+    edges = [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 512, 1000, 2047, 2048, 2049, 4096, 8191, 8192, 8193]
+    for M in edges:
+        for N in edges:
+            for K in (128, 1920, 2048, 2176, 7168):
+                assert _moe._split_workspace(M, N, K) == ws(M, N, K), (M, N, K)
