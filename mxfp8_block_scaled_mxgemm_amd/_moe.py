@@ -370,7 +370,8 @@ def _linear(a, a_scale, w, w_scale, bias, act, gated, residual, offsets, mode, o
     if work:
         work_mem = torch.empty(work, dtype=torch.uint8, device=dev)
         work_ptr = work_mem.data_ptr()
-    w_group, w_scale_group = (w.stride(0), w_scale.stride(0)) if by_row else (0, 0)
+    # (the only expert's stride may be anything)
+    w_group, w_scale_group = (w.stride(0), w_scale.stride(0)) if by_row and E > 1 else (0, 0)
     _run(_load().mxgemm_linear, dev, LINEAR_ARGS.pack(
         a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias_ptr, res_ptr, out.data_ptr(),
         scale_ptr, z_ptr, off, M, N, K, lda, lda_s, ldw, ldw_s, w_group, w_scale_group, ld_res, cols, M * cols,

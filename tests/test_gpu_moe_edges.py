@@ -256,6 +256,17 @@ def test_stores_past_32_bits():
 
 # ---------------------------------------------------------------- products --
 
+@pytest.mark.parametrize("stride", [0, 1, 5, 64 * 256 + 3])
+def test_stride_of_the_only_expert_does_not_matter(stride):
+    torch_cuda()
+    M, N, K = 40, 64, 256
+    g = torch.Generator().manual_seed(2)
+    a, a_s, w, w_s = (t.cuda() for t in (*mc.codes(g, (M, K), "e4m3"), *mc.codes(g, (N, K), "e4m3")))
+    say(f"one expert, stride {stride}")
+    offsets = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    lone = lambda t: torch.as_strided(t, (1, *t.shape), (stride, t.shape[1], 1))  # noqa: E731
+    assert torch.equal(pkg.linear(a, a_s, lone(w), lone(w_s), offsets=offsets), pkg.linear(a, a_s, w, w_s))
+
 TILES = {0: False, 1: True, 2: True, 3: True, 4: True}      # configuration: has it an exact kernel
 
 
