@@ -12,7 +12,8 @@
  * GPU can access; anything else is refused with MXGEMM_EINVAL) and must stay
  * valid until the work completes; buffer sizes are the caller's contract, and
  * so is that no output overlaps another operand.
- * Results do not depend on timing: no sum is formed by atomics.
+ * Results do not depend on timing: no floating-point sum is formed by atomics
+ * (the sort adds whole numbers with them).
  *
  * MXFP8 here is as in mxgemm_seg.h: FP8 codes (E4M3 or E5M2) in blocks of 32
  * along the inner axis with one E8M0 scale byte each, value = fp8(q) *

@@ -66,8 +66,10 @@ struct Raw16 {
 // last one count as zeros, so blocks never cross experts.  d_out and z are read
 // once and the two bytes per element written: 4096 x 4096 with gelu_tanh, 31
 // us (103 MB, 3.3 TB/s); 8002 rows of 2 x 1024 gated with silu over 24
-// experts, 31 us (86 MB, 2.8 TB/s).  Bound by instructions: two quantisations
-// and the activation's slope per element.
+// experts, 33 us (92 MB, 2.8 TB/s).  Bound by instructions: two quantisations
+// and the activation's slope per element.  Without VEC a row's loads wait for
+// the row before: 4096 x 4096 FP32 with silu 28 us (bfloat16 24 in the same
+// loop), 4096 rows of 2 x 1041 gated 40 us.
 constexpr int kGradRows = 128, kGradCols = 64;
 
 // Place of (tile column, row) in LDS: spread so that neither eight columns 8

@@ -944,8 +944,8 @@ __device__ __forceinline__ void groups_partial(const LinArgs& p, uint8_t* lds, v
 // free: the accumulators go through LDS in slabs of 32 rows x 64 columns, so
 // that bias, activation, residual and the stores run on whole rows; the K
 // groups' slabs are added there in group order.  Measured, with what bounds
-// them: 256 x 256 native, 8192 x 8192 x 8192 with bias, silu and residual, 485
-// us (the K loop's copies; the epilogue 5%); 128 x 128 native by expert, 16384
+// them: 256 x 256 native, 8192 x 8192 x 8192 with bias, silu and residual, 475
+// us (the K loop; its copies are about 100 us of it, the epilogue 5%); 128 x 128 native by expert, 16384
 // rows of 4096 x 4096 over 32 experts, gated silu to MXFP8, 395 us, 1.40
 // PFLOP/s (the same copies, twice the bytes per product, and tiles that end
 // early: 11% of their rows); by inner range, exact, 24 experts of 384 tokens,

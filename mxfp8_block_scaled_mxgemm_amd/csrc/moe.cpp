@@ -178,7 +178,10 @@ int check_stride(const char* name, int64_t ld, int64_t cols)
 // with more rows than the tile reads its weights again, so from 8 rows per
 // expert on the 128 x 128 tiles stream them better (native, 64 x 8 over 64,
 // 4096 x 4096: 250 us against 351; exact, 299 against 356).  Dense, 32 x 2048
-// x 7168: 17.8 against 21.9 us with 64 x 64 tiles; 64 rows: 31 against 24 us.
+// x 7168: 17.8 against 21.9 us with 64 x 64 tiles whose K is not split; 64 rows:
+// 31 against 24 us.  (With K split, which needs a workspace and is offered from
+// 33 rows on, 33 rows take 16.7 us and 64 rows 17.2, where 32 take 18.5 and 16
+// take 14.5: between 17 and 32 rows of a long K the limit is not the best one.)
 // Otherwise 128 x 128 tiles, two of whose work-groups share a compute unit (the
 // epilogue of one runs beside the K loop of the other), where they occupy more
 // than half of the compute units (1024 x 2048 x 4096, 128 tiles: 35 against 31
