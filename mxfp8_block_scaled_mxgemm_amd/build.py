@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libmxgemm_seg.so")
 SOURCES = ["kernels.hip", "gemm_e4m3_e4m3.hip", "gemm_e5m2_e5m2.hip", "gemm_e4m3_e5m2.hip",
            "gemm_e5m2_e4m3.hip", "ring.hip", "mxgemm_seg.cpp", "tokens.hip", "grad.hip", "layout.hip", "linear_finish.hip",
            "linear_e4m3_e4m3.hip", "linear_e5m2_e5m2.hip", "linear_e4m3_e5m2.hip",
-           "linear_e5m2_e4m3.hip", "moe.cpp"]
+           "linear_e5m2_e4m3.hip", "moe.cpp", "route.hip", "norm.hip", "block_quant.hip", "block_e4m3_e4m3.hip",
+           "block_e5m2_e5m2.hip", "block_e4m3_e5m2.hip", "block_e5m2_e4m3.hip", "block.cpp"]
 ARCH = "gfx950"
 
 # Packed-FP32 ALU forms are switched off for every kernel (the compiler would

@@ -1,0 +1,6 @@
+// The product's kernels with scales of 128 for A E4M3, W E5M2.
+#include "block_impl.h"
+
+namespace mxg {
+template hipError_t launch_block_fmt<kE4M3, kE5M2>(int, bool, const BlockLinArgs&, hipStream_t);
+}

@@ -1,0 +1,381 @@
+// FP8 codes with a float32 scale for each block of 128, along the rows, along
+// the columns and in squares.
+#include "activation.h"
+#include "block.h"
+#include "element.h"
+#include "quant.h"
+#include "segments.h"
+#include "wave.h"
+
+namespace mxg {
+
+// A block's scale and what its elements are multiplied by.  The scale is the
+// largest magnitude over the format's, at least 2^-126 so that its reciprocal
+// is a number; a block that holds a NaN or an infinity has a NaN scale and NaN
+// codes, since no scale represents it.  The codes are rounded from y (fmax /
+// amax), one FP32 rounding of the factor and one of the product away from y / s.
+struct BlockScale {
+    float s, mul;
+    bool nan;
+};
+
+template <int F>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits)
+{
+    constexpr float kMax = F == kE5M2 ? 57344.f : 448.f;
+    constexpr float kLow = 1.1754943508222875e-38f;     // 2^-126
+    const float amax = __uint_as_float(amax_bits);
+    BlockScale b;
+    b.nan = amax_bits >= 0x7F800000u;
+    const bool low = amax <= kMax * kLow;
+    b.s = b.nan ? __uint_as_float(0x7FC00000u) : low ? kLow : amax / kMax;
+    b.mul = low ? 8.507059173023462e37f : kMax / amax;  // 2^126
+    return b;
+}
+
+// Codes of four elements, first in the low byte; round to nearest even.  (The
+// product of the block's largest element may come out a step over fmax.)
+template <int F>
+__device__ __forceinline__ uint32_t block_codes(const BlockScale& b, float x, float y, float z, float w)
+{
+    constexpr float kMax = F == kE5M2 ? 57344.f : 448.f;
+    x = __builtin_amdgcn_fmed3f(x * b.mul, -kMax, kMax);
+    y = __builtin_amdgcn_fmed3f(y * b.mul, -kMax, kMax);
+    z = __builtin_amdgcn_fmed3f(z * b.mul, -kMax, kMax);
+    w = __builtin_amdgcn_fmed3f(w * b.mul, -kMax, kMax);
+    int c;
+    if constexpr (F == kE5M2) {
+        c = __builtin_amdgcn_cvt_pk_bf8_f32(x, y, 0, false);
+        c = __builtin_amdgcn_cvt_pk_bf8_f32(z, w, c, true);
+    } else {
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(x, y, 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(z, w, c, true);
+    }
+    return b.nan ? 0x7F7F7F7Fu : (uint32_t)c;
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// ------------------------------------------------------------------- tile ----
+
+// A work-group of 256 threads takes a tile of 128 rows x 128 columns: lane
+// group l = tid % 16 columns 8 l .. 8 l + 7, thread group r = tid / 16 rows
+// 8 r .. 8 r + 7.  A block along the columns is then sixteen neighbouring
+// lanes; one along the rows is the sixteen thread groups, whose maxima meet in
+// LDS.  A thread's eight rows of a column are eight bytes of the transposed
+// codes; the tile of those goes through LDS so that whole columns of 128 bytes
+// are written.
+constexpr int kTile = 128;
+constexpr int kTileRow = kTile + 16;        // bytes between columns in LDS: 16-byte pieces, spread over the banks
+
+struct TileLds {
+    uint32_t amax[4][kTile];
+    uint8_t codes[kTile * kTileRow];
+};
+
+// Codes along the columns of the thread's rows [row0 + 8 r, ..) below `end`;
+// those from `live` on are zero, codes and scales.
+template <int F>
+__device__ __forceinline__ void put_rows8(const float (&v)[8][8], uint8_t* q, int64_t ld_q, float* s, int64_t ld_s,
+                                          int64_t row, int64_t end, int64_t live, int tc, int tid)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            m = max(m, magnitude(v[i][u]));
+        const BlockScale b = block_scale<F>(row16_max(m));
+        if (row + i < end) {
+            *reinterpret_cast<u32x2*>(q + (row + i) * ld_q + tc * kTile + 8 * (tid & 15)) =
+                u32x2{block_codes<F>(b, v[i][0], v[i][1], v[i][2], v[i][3]),
+                      block_codes<F>(b, v[i][4], v[i][5], v[i][6], v[i][7])};
+            if ((tid & 15) == 0)
+                s[tc * ld_s + row + i] = row + i < live ? b.s : 0.f;
+        }
+    }
+}
+
+// The eight columns' maxima over the tile's 128 rows.
+__device__ __forceinline__ void column_max(const float (&v)[8][8], TileLds& lds, uint32_t (&m)[8], int tid)
+{
+    const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        m[u] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m[u] = max(m[u], magnitude(v[i][u]));
+        m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 16));
+        m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 32));
+    }
+    if (lane < 16)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            lds.amax[wave][8 * lane + u] = m[u];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int c = 8 * (tid & 15) + u;
+        m[u] = max(max(lds.amax[0][c], lds.amax[1][c]), max(lds.amax[2][c], lds.amax[3][c]));
+    }
+}
+
+template <int F>
+__device__ __forceinline__ void flip(const float (&v)[8][8], const BlockScale& b, int u, TileLds& lds, int tid)
+{
+    *reinterpret_cast<u32x2*>(lds.codes + (8 * (tid & 15) + u) * kTileRow + 8 * (tid >> 4)) =
+        u32x2{block_codes<F>(b, v[0][u], v[1][u], v[2][u], v[3][u]),
+              block_codes<F>(b, v[4][u], v[5][u], v[6][u], v[7][u])};
+}
+
+// The transposed codes out of LDS: column c of the tile, below `cols`, to row
+// c of out.
+__device__ __forceinline__ void put_columns(const TileLds& lds, uint8_t* out, int64_t ld, int cols, int tid)
+{
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = 32 * k + (tid >> 3), at = 16 * (tid & 7);
+        if (c < cols)
+            *reinterpret_cast<u32x4*>(out + c * ld + at) = *reinterpret_cast<const u32x4*>(lds.codes + c * kTileRow + at);
+    }
+}
+
+// ----------------------------------------------------------- activations ----
+
+// Eight columns of one row of y, from column c on (zero past C).
+template <int TYPE, bool BACK>
+__device__ __forceinline__ void value8(const BlockQuantArgs& p, int64_t row, int c, float (&v)[8])
+{
+    const int half = p.half;
+    if constexpr (!BACK) {
+        if (!half) {
+            load8<TYPE>(p.x, row * p.ld_x, c, p.C, v);
+            activate(p.act, v);
+        } else {
+            float u[8];
+            load8<TYPE>(p.x, row * p.ld_x, c, half, v);
+            load8<TYPE>(p.x, row * p.ld_x + half, c, half, u);
+            activate(p.act, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] *= u[i];
+        }
+    } else {
+        // the columns as [first, first + 8) of one half; a piece that reaches
+        // over the middle is taken a column at a time
+        const bool up = half && c >= half;
+        if (!half || up || c + 8 <= half) {
+            const int width = half ? half : p.C, first = up ? c - half : c;
+            float z[8], z1[8], y[8];
+            load8<TYPE>(p.x, row * p.ld_x, first, width, v);
+            load8<kBF16>(p.z, row * p.ld_z, first, width, z);
+            if (half && !up)
+                load8<kBF16>(p.z, row * p.ld_z + half, first, width, z1);
+            activate_grads(p.act, z, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] *= !half ? z[i] : up ? y[i] : z[i] * z1[i];
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < 8 && c + i < p.C; ++i) {
+            const bool hi = c + i >= half;
+            const int col = hi ? c + i - half : c + i;
+            float d[8], z[8], z1[8], y[8];
+            load8<TYPE>(p.x, row * p.ld_x, col, col + 1, d);
+            load8<kBF16>(p.z, row * p.ld_z, col, col + 1, z);
+            load8<kBF16>(p.z, row * p.ld_z + half, col, col + 1, z1);
+            activate_grads(p.act, z, y);
+            const float one = d[0] * (hi ? y[0] : z[0] * z1[0]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = j == i ? one : v[j];
+        }
+    }
+}
+
+// By expert, what no segment holds is zero: the rows of dropped pairs, and
+// the columns of qt past the last segment.
+__device__ __forceinline__ void clear_rest(const BlockQuantArgs& p, int chunk, int tc)
+{
+    const int tid = threadIdx.x;
+    const int64_t Cp = (p.C + kTile - 1) / kTile * kTile;
+    if (p.qt && chunk < p.chunks) {
+        const int cols = p.C - tc * kTile < kTile ? p.C - tc * kTile : kTile;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = 32 * k + (tid >> 3);
+            if (c < cols)
+                *reinterpret_cast<u32x4*>(p.qt + (tc * kTile + c) * p.ld_qt + (int64_t)chunk * kTile + 16 * (tid & 7)) =
+                    u32x4{0, 0, 0, 0};
+        }
+        if (tid < cols)
+            p.st[(int64_t)chunk * p.C + tc * kTile + tid] = 0.f;
+    }
+    if (!p.q)
+        return;
+    // the chunks past the last segment share the dropped rows
+    int first = p.k_offsets[p.groups], live = p.offsets[p.groups];
+    first = first < 0 ? 0 : (first + kTile - 1) / kTile;
+    first = first < p.chunks ? first : p.chunks;
+    live = live < 0 ? 0 : live;
+    const int64_t stride = (int64_t)(p.chunks + 1 - first) * 32;
+    for (int64_t row = live + (int64_t)(chunk - first) * 32 + (tid >> 3); row < p.rows; row += stride) {
+        *reinterpret_cast<u32x4*>(p.q + row * Cp + tc * kTile + 16 * (tid & 7)) = u32x4{0, 0, 0, 0};
+        if ((tid & 7) == 0)
+            p.s[(int64_t)tc * p.rows + row] = 0.f;
+    }
+}
+
+template <int F, int TYPE, bool BACK>
+__global__ void __launch_bounds__(256) block_quant_kernel(BlockQuantArgs p)
+{
+    __shared__ TileLds lds;
+    const int tid = threadIdx.x, tc = blockIdx.x, chunk = blockIdx.y;
+    int row0 = chunk * kTile, end = p.rows, live = p.rows;
+    if (!p.qt) {        // rows in any order: no segments, the dropped ones last
+        if (p.offsets)
+            live = min(max(p.offsets[p.groups], 0), p.rows);
+    } else {
+        if (!segment_rows(p, chunk, row0, end)) {
+            clear_rest(p, chunk, tc);
+            return;
+        }
+        live = end;
+    }
+    const int c = tc * kTile + 8 * (tid & 15);
+    const int64_t row = row0 + 8 * (tid >> 4);
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (row + i < live) {
+            value8<TYPE, BACK>(p, row + i, c, v[i]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[i][u] = 0.f;
+        }
+    }
+    if (p.q)
+        put_rows8<F>(v, p.q, (int64_t)(p.C + kTile - 1) / kTile * kTile, p.s, p.rows, row, end, live, tc, tid);
+    if (!p.qt)
+        return;
+    uint32_t m[8];
+    column_max(v, lds, m, tid);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const BlockScale b = block_scale<F>(m[u]);
+        flip<F>(v, b, u, lds, tid);
+        if (tid < 16 && c + u < p.C)
+            p.st[(int64_t)chunk * p.C + c + u] = b.s;
+    }
+    const int cols = p.C - tc * kTile;
+    put_columns(lds, p.qt + (int64_t)tc * kTile * p.ld_qt + (int64_t)chunk * kTile, p.ld_qt, cols, tid);
+}
+
+// ---------------------------------------------------------------- squares ----
+
+template <int F, int TYPE>
+__global__ void __launch_bounds__(256) square_quant_kernel(SquareQuantArgs p)
+{
+    __shared__ TileLds lds;
+    const int tid = threadIdx.x, tk = blockIdx.x, tn = blockIdx.y;
+    const int64_t e = blockIdx.z;
+    const int kb = gridDim.x, nb = gridDim.y;
+    const int c = tk * kTile + 8 * (tid & 15), row = tn * kTile + 8 * (tid >> 4);
+    float v[8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (row + i < p.N) {
+            load8<TYPE>(p.w, e * p.group + (row + i) * p.ld, c, p.K, v[i]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[i][u] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            m = max(m, magnitude(v[i][u]));
+    m = wave_max(m);
+    if ((tid & 63) == 0)
+        lds.amax[0][tid >> 6] = m;
+    __syncthreads();
+    m = max(max(lds.amax[0][0], lds.amax[0][1]), max(lds.amax[0][2], lds.amax[0][3]));
+    const BlockScale b = block_scale<F>(m);
+    if (tid == 0) {
+        p.s[(e * nb + tn) * kb + tk] = b.s;
+        if (p.qt)
+            p.st[(e * kb + tk) * nb + tn] = b.s;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (row + i < p.N)
+            *reinterpret_cast<u32x2*>(p.q + ((e * p.N + row + i) * kb + tk) * kTile + 8 * (tid & 15)) =
+                u32x2{block_codes<F>(b, v[i][0], v[i][1], v[i][2], v[i][3]),
+                      block_codes<F>(b, v[i][4], v[i][5], v[i][6], v[i][7])};
+    if (!p.qt)
+        return;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        flip<F>(v, b, u, lds, tid);
+    const int64_t ld = (int64_t)nb * kTile;
+    put_columns(lds, p.qt + (e * p.K + (int64_t)tk * kTile) * ld + (int64_t)tn * kTile, ld, p.K - tk * kTile, tid);
+}
+
+// ----------------------------------------------------------------- launch --
+
+template <int F, int TYPE>
+static void quant_launch(const BlockQuantArgs& a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((a.C + kTile - 1) / kTile), (unsigned)a.chunks + (a.qt && a.offsets ? 1 : 0));
+    if (a.z)
+        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, true>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, false>), grid, dim3(256), 0, stream, a);
+}
+
+template <int F>
+static hipError_t quant_launch(const BlockQuantArgs& a, hipStream_t stream)
+{
+    if (a.type == kBF16)
+        quant_launch<F, kBF16>(a, stream);
+    else if (a.type == kFP16)
+        quant_launch<F, kFP16>(a, stream);
+    else
+        quant_launch<F, kFP32>(a, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_block_quant(const BlockQuantArgs& a, hipStream_t stream)
+{
+    return a.fmt == kE5M2 ? quant_launch<kE5M2>(a, stream) : quant_launch<kE4M3>(a, stream);
+}
+
+template <int F>
+static hipError_t square_launch(const SquareQuantArgs& a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((a.K + kTile - 1) / kTile), (unsigned)((a.N + kTile - 1) / kTile), (unsigned)a.batch);
+    if (a.type == kBF16)
+        hipLaunchKernelGGL((square_quant_kernel<F, kBF16>), grid, dim3(256), 0, stream, a);
+    else if (a.type == kFP16)
+        hipLaunchKernelGGL((square_quant_kernel<F, kFP16>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((square_quant_kernel<F, kFP32>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_square_quant(const SquareQuantArgs& a, hipStream_t stream)
+{
+    return a.fmt == kE5M2 ? square_launch<kE5M2>(a, stream) : square_launch<kE4M3>(a, stream);
+}
+
+}  // namespace mxg

@@ -51,6 +51,35 @@ struct Pack {
     }
 };
 
+// Eight consecutive columns [c, c + 8) of row `at` of an [.., n] array as
+// FP32; zero past n.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int c, int n, float (&v)[8])
+{
+    const typename Element<TYPE>::T* p = static_cast<const typename Element<TYPE>::T*>(base) + at + c;
+    if (c + 8 <= n) {
+        Pack<TYPE, 8> x;
+        x.load(p);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[u] = x.get(u);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[u] = c + u < n ? Element<TYPE>::get(p[u]) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void load8(int type, const void* base, int64_t at, int c, int n, float (&v)[8])
+{
+    if (type == kBF16)
+        load8<kBF16>(base, at, c, n, v);
+    else if (type == kFP16)
+        load8<kFP16>(base, at, c, n, v);
+    else
+        load8<kFP32>(base, at, c, n, v);
+}
+
 // A row of `cols` elements as pieces of V: the last one is moved back to
 // end with the row (it then repeats elements of the piece before it).
 template <int V>

@@ -4,37 +4,9 @@
 #include "linear.h"
 #include "quant.h"
 #include "schedule.h"
+#include "segments.h"
 
 namespace mxg {
-
-// Eight consecutive columns [c, c + 8) of row `at` of an [.., n] array as
-// FP32; zero past n.
-template <int TYPE>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int c, int n, float (&v)[8])
-{
-    const typename Element<TYPE>::T* p = static_cast<const typename Element<TYPE>::T*>(base) + at + c;
-    if (c + 8 <= n) {
-        Pack<TYPE, 8> x;
-        x.load(p);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            v[u] = x.get(u);
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            v[u] = c + u < n ? Element<TYPE>::get(p[u]) : 0.f;
-    }
-}
-
-__device__ __forceinline__ void load8(int type, const void* base, int64_t at, int c, int n, float (&v)[8])
-{
-    if (type == kBF16)
-        load8<kBF16>(base, at, c, n, v);
-    else if (type == kFP16)
-        load8<kFP16>(base, at, c, n, v);
-    else
-        load8<kFP32>(base, at, c, n, v);
-}
 
 // Eight 16-bit elements as loaded.
 struct Raw16 {
@@ -79,33 +51,6 @@ constexpr int kGradWords = 132 * kGradCols + 64;
 __device__ __forceinline__ int grad_at(int col, int row)
 {
     return 132 * col + 8 * (col >> 3) + 4 * (col >> 5) + row + (row >> 5);
-}
-
-// First token of a chunk of 128 and the end of its expert; false past the
-// last segment (and past the last chunk, whatever k_offsets holds).
-__device__ __forceinline__ bool grad_rows(const GradArgs& p, int chunk, int& row0, int& end)
-{
-    row0 = chunk * kGradRows;
-    end = p.rows;
-    if (!p.offsets)
-        return true;
-    // the expert whose padded segment holds this chunk
-    const int at = row0;
-    if (chunk >= p.chunks || at >= p.k_offsets[p.groups])
-        return false;
-    int lo = 0, hi = p.groups;              // k_offsets[lo] <= at < k_offsets[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.k_offsets[mid] <= at)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    row0 = p.offsets[lo] + at - p.k_offsets[lo];
-    end = p.offsets[lo + 1];
-    end = end < p.rows ? end : p.rows;
-    row0 = row0 < 0 ? 0 : row0;
-    return true;
 }
 
 // By expert, what no segment holds is zero: the rows of dropped pairs, and the
@@ -222,7 +167,7 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs p)
     const int tid = threadIdx.x, lane = tid & 63;
     const int chunk = blockIdx.y;
     int row0, end;
-    if (!grad_rows(p, chunk, row0, end)) {
+    if (!segment_rows(p, chunk, row0, end)) {
         grad_rest(p, chunk, blockIdx.x * kGradCols);
         return;
     }

@@ -7,13 +7,15 @@
 #include <math.h>
 #include <string.h>
 
-#include <atomic>
-
 #include "host_util.h"
 #include "linear.h"
 #include "moe.h"
 #include "schedule.h"
 
+using mxg::Buffer;
+using mxg::check_buffers;
+using mxg::check_stride;
+using mxg::current_device;
 using mxg::fail;
 
 namespace mxg {
@@ -48,54 +50,6 @@ LinTile lin_tile(int cfg, const LinArgs& a)
 }  // namespace mxg
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-// Compute units of the current device, which must be a gfx950; looked up
-// once per device.
-int current_device(int* dev, int* cus)
-{
-    static std::atomic<int> known[kMaxDevices];     // 0: not looked up, else compute units
-    HIP_TRY(hipGetDevice(dev));
-    if (*dev < 0 || *dev >= kMaxDevices)
-        return fail(MXGEMM_EUNSUPPORTED, "device index %d out of range", *dev);
-    *cus = known[*dev].load(std::memory_order_relaxed);
-    if (*cus == 0) {
-        hipDeviceProp_t prop;
-        HIP_TRY(hipGetDeviceProperties(&prop, *dev));
-        if (strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-            return fail(MXGEMM_EUNSUPPORTED, "device %d is %s; this library is built for gfx950", *dev,
-                        prop.gcnArchName);
-        *cus = prop.multiProcessorCount;
-        known[*dev].store(*cus, std::memory_order_relaxed);
-    }
-    return MXGEMM_OK;
-}
-
-struct Buffer {
-    const void* p;
-    const char* name;
-    int align;
-    bool optional;
-};
-
-template <size_t N>
-int check_buffers(const Buffer (&b)[N], int dev)
-{
-    for (const Buffer& x : b) {
-        if (!x.p) {
-            if (x.optional)
-                continue;
-            return fail(MXGEMM_EINVAL, "%s is NULL", x.name);
-        }
-        if ((uintptr_t)x.p % x.align != 0)
-            return fail(MXGEMM_EINVAL, "%s must be %d-byte aligned", x.name, x.align);
-        const int rc = mxg::gpu_accessible(x.p, x.name, dev);
-        if (rc != MXGEMM_OK)
-            return rc;
-    }
-    return MXGEMM_OK;
-}
 
 int element_size(int type) { return type == MXGEMM_TYPE_FP32 ? 4 : 2; }
 
@@ -154,21 +108,6 @@ int token_args(mxg::TokenArgs* a, int32_t type, int64_t tokens, int32_t k, int64
     a->row_of = row_of;
     return MXGEMM_OK;
 }
-
-int check_stride(const char* name, int64_t ld, int64_t cols)
-{
-    if (ld < cols)
-        return fail(MXGEMM_EINVAL, "row stride %lld of %s is less than its %lld columns", (long long)ld, name,
-                    (long long)cols);
-    return MXGEMM_OK;
-}
-
-#define TRY(expr)                 \
-    do {                          \
-        const int rc_ = (expr);   \
-        if (rc_ != MXGEMM_OK)     \
-            return rc_;           \
-    } while (0)
 
 // -------------------------------------------------------------- product ----
 
