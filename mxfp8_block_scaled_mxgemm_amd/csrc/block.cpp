@@ -90,25 +90,42 @@ int route_args(mxg::RouteArgs* a, const void* logits, int64_t ld, int32_t type, 
 
 // ---------------------------------------------------------------- product --
 
-// The tile configuration for a product, and why: as for the MXFP8 products
-// (whose kernels have the same shapes), few rows of an average expert stream
-// the weights, tiles of 128 x 128 where they occupy more than half of the
-// compute units, and 256 x 256 for native dense products of a long K.
+// The tile configuration for a product.  Few rows (of an average expert): the
+// weights' bytes are the cost, and the skinny kernels stream them.  By expert,
+// exact, 4096 x 4096 weights, 16-row / 32-row / 128 x 128 tiles: 8 rows per
+// expert of 64, 195 / 204 / 274 us; 16 of 32, 141 / 116 / 144; 32 of 32, 223 /
+// 172 / 146.  Dense, 32-row tiles against 64 x 64 ones with split K: 32 x 2048 x
+// 7168, 13.4 and 21.9 us; 64 x 2048 x 7168 13.9 and 16.1; 64 x 8192 x 8192, where
+// two row tiles no longer fit on the compute units at once, 36 and 22.
+// Then 128 x 128 tiles, two of whose work-groups share a compute unit, where
+// they occupy more than half of the compute units (512 x 4096 x 4096 exact, 128
+// tiles: 37 us against 29 with 64 x 64 ones).  Native products of squares may
+// take 256 x 256 tiles: a round of those on all compute units takes 5 / 3 of the
+// time of a round of 128 x 128 ones (8192 x 8192 x 8192: 464 us in 4 rounds and
+// 562 in 8), so the rule compares rounds; the experts' last tiles count half.
+// 2048 x 4096 x 4096: 55 and 44 us; 2048 x 8192 x 2048: 40 and 45; 3000 x 4096 x
+// 2048: 35 and 37; 4096 x 4096 x 512: 20 and 21; by expert, 4096 x 4096 weights:
+// 32 of 128 rows 219 and 180, 64 of 256 423 and 484, 32 of 512 430 and 430.
 int choose_tile(const mxg::BlockLinArgs& a, bool exact, int cus)
 {
     const bool by = a.mode == mxg::kByRows;
     const int64_t r = by ? (a.rows + a.groups - 1) / a.groups : a.rows;
-    if (a.squares && r <= (by ? 6 : 16))
+    if (a.squares && r <= (by ? 10 : 16))
         return mxg::kBlockRows16;
-    if (a.squares && r <= 32 && !by)
+    if (a.squares && (r <= (by ? 24 : 32) || (!by && r <= 64 && (r + 31) / 32 * ((a.N + 15) / 16) <= cus)))
         return mxg::kBlockRows32;
-    auto tiles = [&](int64_t m, int64_t n) {
-        return (a.mode == mxg::kDense ? 1 : a.groups) * ((r + m - 1) / m) * ((a.N + n - 1) / n);
+    // tiles of m x n, twice (an expert ends inside its last one)
+    auto tiles2 = [&](int64_t m, int64_t n) {
+        const int64_t rows = by ? (2 * r + m) / m * a.groups : 2 * ((r + m - 1) / m);
+        return (a.mode == mxg::kByInner ? a.groups : 1) * rows * ((a.N + n - 1) / n);
     };
-    if (!exact && a.squares && a.K >= 2048 &&
-        (a.mode == mxg::kDense ? tiles(256, 256) >= cus : by && r >= 1024 && tiles(256, 256) >= 4 * cus))
-        return mxg::kBlock256x256;
-    return tiles(128, 128) > cus / 2 ? mxg::kBlock128x128 : mxg::kBlock64x64;
+    const int64_t big = tiles2(256, 256), mid = tiles2(128, 128);
+    if (!exact && a.squares) {
+        const int64_t cost_big = 5 * ((big + 2 * cus - 1) / (2 * cus)), cost_mid = 3 * ((mid + 4 * cus - 1) / (4 * cus));
+        if (cost_big < cost_mid || (cost_big == cost_mid && a.K >= 2048))
+            return mxg::kBlock256x256;
+    }
+    return mid > cus ? mxg::kBlock128x128 : mxg::kBlock64x64;
 }
 
 // K splits of a dense product of 64 x 64 tiles: as many work-groups as
@@ -220,12 +237,12 @@ int plan_linear(mxg::BlockLinArgs* a, int cfg, int cus, int64_t workspace_bytes)
 
 // ------------------------------------------------------------------- norm --
 
-// Rows of the gradient in units, each within one gate row's, and workers.  The
-// workers' partial rows are the workspace.
-constexpr int64_t kNormWorkers = 1024;
-
+// Rows of the gradient in units, each within one gate row's, and workers: at
+// most as many as 16 waves on each of 256 compute units (their registers allow
+// no more).  The workers' partial rows are the workspace.
 void plan_norm(mxg::NormArgs* a, int64_t gate_rows)
 {
+    const int64_t most = 256 * 16 * 64 / mxg::norm_shape(a->cols).threads;
     a->gates = gate_rows;
     a->per_gate = a->rows / gate_rows;
     a->units = 1;
@@ -233,14 +250,14 @@ void plan_norm(mxg::NormArgs* a, int64_t gate_rows)
         a->units = a->per_unit = a->workers = 0;
         return;
     }
-    if (gate_rows < kNormWorkers) {
-        a->units = kNormWorkers / gate_rows;
+    if (gate_rows < most) {
+        a->units = most / gate_rows;
         a->units = a->units < a->per_gate ? a->units : a->per_gate;
     }
     a->per_unit = (a->per_gate + a->units - 1) / a->units;
     a->units = (a->per_gate + a->per_unit - 1) / a->per_unit;
     const int64_t all = gate_rows * a->units;
-    a->workers = (int)(all < kNormWorkers ? all : kNormWorkers);
+    a->workers = (int)(all < most ? all : most);
 }
 
 int norm_args(const mxgemm_norm_t* g, mxg::NormArgs* a, bool backward)
@@ -505,6 +522,7 @@ int64_t mxgemm_add_norm_workspace(int64_t rows, int64_t cols, int64_t gate_rows)
     mxg::NormArgs a;
     memset(&a, 0, sizeof(a));
     a.rows = rows;
+    a.cols = (int)cols;
     plan_norm(&a, gate_rows);
     return 3LL * a.workers * cols * 4;
 }

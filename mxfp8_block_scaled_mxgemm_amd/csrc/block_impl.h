@@ -107,6 +107,8 @@ struct BlockCopies {
 // Fragments as in the MXFP8 loops: lane l has row l % 32 and, with q = l / 32,
 // the 16-byte chunks 2 c + q of its 128 bytes.  The result of a 32 x 32 block
 // has row l % 32 of a and column 8 (v / 4) + 4 q + v % 4 of w in element v.
+typedef float v8f __attribute__((ext_vector_type(8)));
+
 template <int GA, int GB, bool SQUARES>
 struct BlockScales {
     float a[GA], w[GB][SQUARES ? 1 : 16];
@@ -133,15 +135,25 @@ struct BlockScales {
     }
     __device__ __forceinline__ void add(v16f& total, const v16f& part, int i, int g) const
     {
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            total[v] += part[v] * (a[i] * w[g][SQUARES ? 0 : v]);
+    }
+    // elements [8 HALF, 8 HALF + 8) of block (i, g)
+    template <int HALF>
+    __device__ __forceinline__ void add_half(v8f& total, const v16f& part, int i, int g) const
+    {
+        v8f x;
+        if constexpr (HALF == 0)
+            x = __builtin_shufflevector(part, part, 0, 1, 2, 3, 4, 5, 6, 7);
+        else
+            x = __builtin_shufflevector(part, part, 8, 9, 10, 11, 12, 13, 14, 15);
         if constexpr (SQUARES) {
-            const float s = a[i] * w[g][0];
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-                total[v] += part[v] * s;
+            total += x * (a[i] * w[g][0]);
         } else {
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-                total[v] += part[v] * (a[i] * w[g][v]);
+            constexpr int f = 8 * HALF;
+            const v8f y = {w[g][f], w[g][f + 1], w[g][f + 2], w[g][f + 3], w[g][f + 4], w[g][f + 5], w[g][f + 6], w[g][f + 7]};
+            total += x * (y * a[i]);
         }
     }
 };
@@ -218,6 +230,124 @@ __device__ __forceinline__ void block_step(const uint8_t* a, const uint8_t* w, c
     }
 }
 
+// ------------------------------------------------------------ native K loop --
+
+// The K loop of tiles of several waves on the FP8 matrix unit, in slots of one
+// MFMA (32 x 32 x 64; two of them, one on the other, make a block's inner
+// sum).  While a slot's MFMA runs, the wave issues eight multiply-adds of the
+// sum before, and its share of the LDS reads and copies: the next 32 rows'
+// fragments of a, and, past the one barrier of a K-step, which comes before
+// the last 32 rows' MFMAs (by then every wave holds all of step s in
+// registers, and step s + 1 has landed), the first fragments and the scales of
+// step s + 1 and the copies of step s + 2.  So neither the barrier nor an LDS
+// read's latency stands between two MFMAs of a wave, and with two waves per
+// SIMD the other one's fill what is left.
+template <int GA, int GB, bool SQUARES, int FA, int FB, class Copies, class Src>
+__device__ __forceinline__ void native_block_loop(const Copies& co, const Src& src_at, uint8_t* lds, int nsteps, int wl,
+                                                  int a_row, int w_row, int lane, v16f (&acc)[GA][GB])
+{
+    typedef typename Copies::G G;
+    constexpr int kSlots = GA * GB * 2, kRow = GB * 2;      // MFMAs of a K-step, of 32 rows
+    constexpr int kBarrier = kSlots - kRow;                 // the barrier is before this one
+    const int lr = lane & 31, lq = lane >> 5;
+    const int last = nsteps - 1;
+    const float* const scales = reinterpret_cast<const float*>(lds + 2 * G::CODES);
+    constexpr int kScales = G::SCALES / 4;
+    const int a_rows = G::A_BYTES / kBK;                    // scales: a's rows, then w's
+
+    auto frag = [&](int stage, int row, int c) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4*>(lds + stage * G::CODES + (row + lr) * kBK + swz_t<32>(lr, 2 * c + lq) * 16);
+    };
+    auto operand = [](const u32x4& lo, const u32x4& hi) __attribute__((always_inline)) {
+        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    u32x4 w[GB][4], a[2][4];
+    BlockScales<GA, GB, SQUARES> now, next;
+    co.issue_all(src_at(0), lds, 0, wl);
+    co.issue_all(src_at(last < 1 ? last : 1), lds, 1, wl);
+    wait_copies<G::COPIES>();
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < GB; ++g)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            w[g][c] = frag(0, a_rows + w_row + 32 * g, c);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        a[0][c] = frag(0, a_row, c);
+    next.load(scales + a_row, scales + a_rows + w_row, lane);
+    now = next;
+
+    v16f part[2];               // the sum being formed and the one before
+    part[1] = v16f{};           // (the first slots add zero to the last block)
+    v8f total[GA][GB][2];
+#pragma unroll
+    for (int i = 0; i < GA; ++i)
+#pragma unroll
+        for (int g = 0; g < GB; ++g)
+            total[i][g][0] = total[i][g][1] = v8f{};
+    for (int s = 0; s < nsteps; ++s) {
+        const int cur = s & 1, nxt = cur ^ 1;
+        const BlockSrc src1 = src_at(s + 1 < last ? s + 1 : last), src2 = src_at(s + 2 < last ? s + 2 : last);
+        static_for<0, kSlots>([&](auto uc) __attribute__((always_inline)) {
+            constexpr int u = decltype(uc)::value, i = u / kRow, g = u % kRow / 2, m = u % 2, pair = u / 2;
+            if constexpr (u == kBarrier) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+            }
+            v16f& sum = part[pair & 1];
+            __builtin_amdgcn_s_setprio(1);
+            sum = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                operand(w[g][2 * m], w[g][2 * m + 1]), operand(a[i & 1][2 * m], a[i & 1][2 * m + 1]),
+                m == 0 ? v16f{} : sum, FB, FA, 0, kUnitScale, 0, kUnitScale);
+            __builtin_amdgcn_s_setprio(0);
+            // the multiply-adds of the pair before
+            constexpr int before = (pair + GA * GB - 1) % (GA * GB), bi = before / GB, bg = before % GB;
+            if constexpr (u == 2)
+                now = next;     // (the last pair of the step before had its own until here)
+            now.template add_half<m>(total[bi][bg][m], part[(pair & 1) ^ 1], bi, bg);
+            // copies: from the barrier on, the last ones in the next step's
+            // first slots (then of what was step s + 2)
+            constexpr int t = u >= kBarrier ? u - kBarrier : u + kRow;
+            if constexpr (t < G::COPIES) {
+                if constexpr (u >= kBarrier)
+                    co.issue(src2, lds, cur, wl, t);
+                else        // (of the second step again, in the first one)
+                    co.issue(src1, lds, nxt, wl, t);
+            }
+            // fragments
+            if constexpr (i + 1 < GA) {
+                if constexpr (GB == 2)
+                    a[(i + 1) & 1][u % kRow] = frag(cur, a_row + 32 * (i + 1), u % kRow);
+            } else {
+                if constexpr (m == 1) {
+                    w[g][0] = frag(nxt, a_rows + w_row + 32 * g, 0);
+                    w[g][1] = frag(nxt, a_rows + w_row + 32 * g, 1);
+                    w[g][2] = frag(nxt, a_rows + w_row + 32 * g, 2);
+                    w[g][3] = frag(nxt, a_rows + w_row + 32 * g, 3);
+                }
+                if constexpr (u % kRow < 2) {
+                    constexpr int c = 2 * (u % kRow);
+                    a[GA & 1][c] = frag(nxt, a_row, c);
+                    a[GA & 1][c + 1] = frag(nxt, a_row, c + 1);
+                }
+                if constexpr (u % kRow == 2)
+                    next.load(scales + nxt * kScales + a_row, scales + nxt * kScales + a_rows + w_row, lane);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+    now.template add_half<0>(total[GA - 1][GB - 1][0], part[1], GA - 1, GB - 1);
+    now.template add_half<1>(total[GA - 1][GB - 1][1], part[1], GA - 1, GB - 1);
+#pragma unroll
+    for (int i = 0; i < GA; ++i)
+#pragma unroll
+        for (int g = 0; g < GB; ++g)
+            acc[i][g] = __builtin_shufflevector(total[i][g][0], total[i][g][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12,
+                                                13, 14, 15);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy outlives the work-group
+}
+
 // ------------------------------------------------------------------ kernel --
 
 // One BM x BN tile per work-group, WGK K groups of WGM x WGN waves.  Two
@@ -278,6 +408,9 @@ block_linear_kernel(BlockLinArgs p)
             return BlockSrc{src0.a + (int64_t)s * kBK, src0.w + (int64_t)s * kBK, src0.as + s * p.as_k * 4,
                             src0.ws + s * p.ws_k * 4};
         };
+        if constexpr (BM == 256) {
+            native_block_loop<GA, GB, SQUARES, FA, FB>(co, src_at, mem, nsteps, wl, wm * TM, wn * TN, lane, acc);
+        } else {
         if (nsteps > 0)
             co.issue_all(src_at(0), mem, 0, wl);
         for (int s = 0; s < nsteps; ++s) {
@@ -292,6 +425,7 @@ block_linear_kernel(BlockLinArgs p)
                                                        sc + wm * TM, sc + BM + wn * TN, lane, acc);
             if constexpr (NWG == 1)
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read before it is copied over
+        }
         }
     }
     __syncthreads();        // every wave has read its last fragments

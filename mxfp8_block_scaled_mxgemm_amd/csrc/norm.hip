@@ -8,43 +8,90 @@ namespace mxg {
 // ------------------------------------------------------------------- rows --
 
 // A row's elements as a worker of NT threads holds them: eight per thread,
-// thread t from column 8 t on.  Elements past the row are zero, and neither
-// read nor written.
-template <int TYPE, int NT>
+// thread t from column 8 t on, as loaded.  Elements past the row are zero.
+// WHOLE: rows of whole eights, whose loads go out without a branch (threads
+// past the row read its last eight and put them aside).
+template <int TYPE, bool WHOLE>
 struct RawRow {
-    Pack<TYPE, 8> v;
+    static constexpr int kWords = TYPE == kFP32 ? 8 : 4;
+    typedef typename Element<TYPE>::T T;
+    uint32_t w[kWords];
+
     __device__ __forceinline__ void load(const void* base, int64_t at, int cols, int t)
     {
-        const typename Element<TYPE>::T* p = static_cast<const typename Element<TYPE>::T*>(base) + at + 8 * t;
-        if (8 * t + 8 <= cols) {
-            v.load(p);
+        const T* p = static_cast<const T*>(base) + at;
+        if constexpr (WHOLE) {
+            const bool live = 8 * t < cols;
+            __builtin_memcpy(w, p + (live ? 8 * t : cols - 8), sizeof(w));
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = live ? w[i] : 0;
+        } else if (8 * t + 8 <= cols) {
+            __builtin_memcpy(w, p + 8 * t, sizeof(w));
         } else {
-            v.zero();
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = 0;
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (8 * t + u < cols)
-                    v.v[u] = p[u];
+                if (8 * t + u < cols) {
+                    if constexpr (TYPE == kFP32)
+                        w[u] = __float_as_uint(p[8 * t + u]);
+                    else
+                        w[u / 2] |= (uint32_t)p[8 * t + u] << (16 * (u & 1));
+                }
         }
     }
     __device__ __forceinline__ void store(void* base, int64_t at, int cols, int t) const
     {
-        typename Element<TYPE>::T* p = static_cast<typename Element<TYPE>::T*>(base) + at + 8 * t;
+        T* p = static_cast<T*>(base) + at + 8 * t;
         if (8 * t + 8 <= cols) {
-            v.store(p);
-        } else {
+            __builtin_memcpy(p, w, sizeof(w));
+        } else if constexpr (!WHOLE) {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (8 * t + u < cols)
-                    p[u] = v.v[u];
+                if (8 * t + u < cols) {
+                    if constexpr (TYPE == kFP32)
+                        p[u] = __uint_as_float(w[u]);
+                    else
+                        p[u] = (uint16_t)(w[u / 2] >> (16 * (u & 1)));
+                }
         }
     }
-    __device__ __forceinline__ void zero() { v.zero(); }
-    __device__ __forceinline__ float get(int i) const { return v.get(i); }
-    __device__ __forceinline__ void put(int i, float f) { v.put(i, f); }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            w[i] = 0;
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if constexpr (TYPE == kFP32)
+                f[u] = __uint_as_float(w[u]);
+            else if constexpr (TYPE == kBF16)
+                f[u] = __uint_as_float(u & 1 ? w[u / 2] & 0xFFFF0000u : w[u / 2] << 16);
+            else
+                f[u] = Element<kFP16>::get((uint16_t)(w[u / 2] >> (16 * (u & 1))));
+        }
+    }
+    // rounds to nearest even
+    __device__ __forceinline__ void put(const float (&f)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (TYPE == kFP32)
+                w[i] = __float_as_uint(f[i]);
+            else if constexpr (TYPE == kBF16)
+                w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+            else
+                w[i] = Element<kFP16>::put(f[2 * i]) | (uint32_t)Element<kFP16>::put(f[2 * i + 1]) << 16;
+        }
+    }
 };
 
 // Weights or a gate row, of any element type, as FP32.
-template <int NT>
 __device__ __forceinline__ void load_row(int type, const void* base, int64_t at, int cols, int t, float (&f)[8])
 {
     load8(type, base, at, 8 * t, cols, f);
@@ -120,70 +167,78 @@ struct Worker {
 };
 
 // r = residual + scale gate post(x), rounded to its type; y = pre(r), of the
-// rounded r (what the next block and the gradient have).  A worker takes rows
-// in turn; the next row's loads go out before this row's sums, which are two
-// trips over lanes and LDS.
-template <int TYPE, int NT>
+// rounded r (what the next block and the gradient have).  A worker takes a run
+// of rows; the next row's loads go out before this row's sums, which are two
+// trips over lanes and LDS, and a gate row is loaded where it begins.
+template <int TYPE, int NT, bool WHOLE>
 __global__ void __launch_bounds__(Worker<NT>::kThreads) norm_kernel(NormArgs p)
 {
     __shared__ float lds[Worker<NT>::kLds];
     const int t = threadIdx.x % NT;
     const int64_t workers = (int64_t)gridDim.x * Worker<NT>::kPerGroup;
-    int64_t row = (int64_t)blockIdx.x * Worker<NT>::kPerGroup + (NT == 64 ? threadIdx.x / 64 : 0);
-    if (row >= p.rows)
+    const int64_t worker = (int64_t)blockIdx.x * Worker<NT>::kPerGroup + (NT == 64 ? threadIdx.x / 64 : 0);
+    const int64_t share = p.rows / workers, more = p.rows % workers;
+    int64_t row = worker * share + (worker < more ? worker : more);
+    const int64_t end = row + share + (worker < more ? 1 : 0);
+    if (row >= end)
         return;
     const float inv_n = 1.f / (float)p.cols;
     int turn = 0;
     float post[8], pre[8], gate[8];
     if (p.post)
-        load_row<NT>(p.post_type, p.post, 0, p.cols, t, post);
+        load_row(p.post_type, p.post, 0, p.cols, t, post);
     if (p.pre)
-        load_row<NT>(p.pre_type, p.pre, 0, p.cols, t, pre);
-    RawRow<TYPE, NT> nx, nres;
+        load_row(p.pre_type, p.pre, 0, p.cols, t, pre);
+    int64_t g = 0, left = 0;            // the gate row, and the rows before the next one's
+    if (p.gate) {
+        g = row / p.per_gate - 1;
+        left = 0;
+    }
+    bool first = true;
+    RawRow<TYPE, WHOLE> nx, nres;
     nx.load(p.x, row * p.ld_x, p.cols, t);
     nres.zero();
     if (p.residual)
         nres.load(p.residual, row * p.ld_res, p.cols, t);
-    for (; row < p.rows; row += workers) {
-        const RawRow<TYPE, NT> x = nx, res = nres;
-        if (p.gate)
-            load_row<NT>(p.gate_type, p.gate, row / p.per_gate * p.ld_gate, p.cols, t, gate);
-        const int64_t next = row + workers;
-        if (next < p.rows) {
-            nx.load(p.x, next * p.ld_x, p.cols, t);
-            if (p.residual)
-                nres.load(p.residual, next * p.ld_res, p.cols, t);
+    for (; row < end; ++row) {
+        const RawRow<TYPE, WHOLE> x = nx, res = nres;
+        if (p.gate && left-- == 0) {
+            ++g;
+            left = (first ? p.per_gate - row % p.per_gate : p.per_gate) - 1;
+            first = false;
+            load_row(p.gate_type, p.gate, g * p.ld_gate, p.cols, t, gate);
         }
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = x.get(i);
+        if (row + 1 < end) {
+            nx.load(p.x, (row + 1) * p.ld_x, p.cols, t);
+            if (p.residual)
+                nres.load(p.residual, (row + 1) * p.ld_res, p.cols, t);
+        }
+        float v[8], sum[8];
+        x.get(v);
         if (p.post) {
             const float rstd = centre<NT>(v, p, inv_n, lds, turn, t);
             times(v, rstd, post);
         }
         if (p.gate)
             times(v, 1.f, gate);
-        RawRow<TYPE, NT> out;
+        res.get(sum);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            out.put(i, res.get(i) + p.scale * v[i]);
-            v[i] = out.get(i);
-        }
+        for (int i = 0; i < 8; ++i)
+            sum[i] += p.scale * v[i];
+        RawRow<TYPE, WHOLE> out;
+        out.put(sum);
         out.store(p.r, row * p.ld_r, p.cols, t);
         if (p.pre) {
+            out.get(v);
             const float rstd = centre<NT>(v, p, inv_n, lds, turn, t);
             times(v, rstd, pre);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                out.put(i, v[i]);
+            out.put(v);
             out.store(p.y, row * p.ld_y, p.cols, t);
         }
     }
 }
 
 // Partial or whole sums of one gate row's gradient.
-template <int NT>
 __device__ __forceinline__ void store_gate(const NormArgs& p, int64_t g, const float (&s)[8], int t)
 {
 #pragma unroll
@@ -201,7 +256,6 @@ __device__ __forceinline__ void store_gate(const NormArgs& p, int64_t g, const f
     }
 }
 
-template <int NT>
 __device__ __forceinline__ void store_part(const NormArgs& p, int which, int64_t worker, const float (&s)[8], int t)
 {
     float* out = p.part + ((int64_t)which * p.workers + worker) * p.cols;
@@ -221,9 +275,39 @@ __device__ __forceinline__ void store_part(const NormArgs& p, int which, int64_t
 // formed again from the rows; a worker takes consecutive units of rows, keeps
 // its columns' sums in registers and leaves them as one partial row, which
 // norm_sums_kernel adds in order.
-template <int TYPE, int NT>
-__global__ void __launch_bounds__(Worker<NT>::kThreads) norm_backward_kernel(NormArgs p)
+template <int TYPE, bool WHOLE>
+struct NormInputs {
+    RawRow<TYPE, WHOLE> dy, dr, x, r;
+    __device__ __forceinline__ void load(const NormArgs& p, int64_t row, int t)
+    {
+        load_first(p, row, t);
+        load_second(p, row, t);
+    }
+    __device__ __forceinline__ void load_first(const NormArgs& p, int64_t row, int t)
+    {
+        if (p.d_y) {
+            dy.load(p.d_y, row * p.ld_dy, p.cols, t);
+            r.load(p.r, row * p.ld_r, p.cols, t);
+        }
+    }
+    __device__ __forceinline__ void load_second(const NormArgs& p, int64_t row, int t)
+    {
+        if (p.d_r)
+            dr.load(p.d_r, row * p.ld_dr, p.cols, t);
+        if (p.post || p.gate)
+            x.load(p.x, row * p.ld_x, p.cols, t);
+    }
+};
+
+template <int TYPE, int NT, bool WHOLE>
+__global__ void __launch_bounds__(Worker<NT>::kThreads) __attribute__((amdgpu_waves_per_eu(NT == 64 ? 3 : 4)))
+norm_backward_kernel(NormArgs p)
 {
+    // Sixteen waves per compute unit are 128 registers each.  Where they allow
+    // it, the next row's loads go out a row ahead; where they do not even hold
+    // a row of everything, half of it is loaded between the two norms.
+    constexpr bool kAhead = TYPE != kFP32 && (NT == 64 || (TYPE == kBF16 && NT < 512));
+    constexpr bool kHalves = TYPE == kFP32;
     __shared__ float lds[Worker<NT>::kLds];
     const int t = threadIdx.x % NT;
     const int64_t worker = (int64_t)blockIdx.x * Worker<NT>::kPerGroup + (NT == 64 ? threadIdx.x / 64 : 0);
@@ -234,54 +318,47 @@ __global__ void __launch_bounds__(Worker<NT>::kThreads) norm_backward_kernel(Nor
     const int64_t share = all / p.workers, more = all % p.workers;
     const int64_t u0 = worker * share + (worker < more ? worker : more), u1 = u0 + share + (worker < more ? 1 : 0);
     int turn = 0;
-    float post[8], pre[8], gate[8];
-    float s_post[8], s_pre[8];
+    float post[8], pre[8], gate[8], s_post[8], s_pre[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         s_post[i] = s_pre[i] = 0.f;
     if (p.post)
-        load_row<NT>(p.post_type, p.post, 0, p.cols, t, post);
+        load_row(p.post_type, p.post, 0, p.cols, t, post);
     if (p.pre)
-        load_row<NT>(p.pre_type, p.pre, 0, p.cols, t, pre);
+        load_row(p.pre_type, p.pre, 0, p.cols, t, pre);
     for (int64_t u = u0; u < u1; ++u) {
-        const int64_t g = u / p.units, first = (u % p.units) * p.per_unit;
+        const int64_t g = u / p.units, first = (u - g * p.units) * p.per_unit;
         int64_t row = g * p.per_gate + first;
         const int64_t left = p.per_gate - first, end = row + (left < p.per_unit ? left : p.per_unit);
         float s_gate[8];
+        NormInputs<TYPE, WHOLE> next;
+        if constexpr (kAhead)
+            next.load(p, row, t);
         if (p.gate) {
-            load_row<NT>(p.gate_type, p.gate, g * p.ld_gate, p.cols, t, gate);
+            load_row(p.gate_type, p.gate, g * p.ld_gate, p.cols, t, gate);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 s_gate[i] = 0.f;
         }
         for (; row < end; ++row) {
-            RawRow<TYPE, NT> dr, raw;
+            if constexpr (kHalves)
+                next.load_first(p, row, t);
+            else if constexpr (!kAhead)
+                next.load(p, row, t);
+            NormInputs<TYPE, WHOLE> in = next;
+            if (kAhead && row + 1 < end)
+                next.load(p, row + 1, t);
             float d[8], v[8];
-            dr.zero();
-            if (p.d_r)
-                dr.load(p.d_r, row * p.ld_dr, p.cols, t);
-            RawRow<TYPE, NT> xraw;
-            if (p.post || p.gate)
-                xraw.load(p.x, row * p.ld_x, p.cols, t);
-            if (p.pre && p.d_y) {
-                raw.load(p.d_y, row * p.ld_dy, p.cols, t);
-                RawRow<TYPE, NT> r;
-                r.load(p.r, row * p.ld_r, p.cols, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = r.get(i);
-                    d[i] = raw.get(i);
-                }
+            if (p.d_y) {
+                in.dy.get(d);
+                in.r.get(v);
                 const float rstd = centre<NT>(v, p, inv_n, lds, turn, t);
                 float s[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     v[i] *= rstd;
                     s_pre[i] += d[i] * v[i];
-                }
-                times(d, 1.f, pre);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                    d[i] *= pre[i];
                     s[0] += d[i] * v[i];
                     s[1] += d[i];
                 }
@@ -289,28 +366,31 @@ __global__ void __launch_bounds__(Worker<NT>::kThreads) norm_backward_kernel(Nor
                 const float dot = s[0] * inv_n, mean = p.layer ? s[1] * inv_n : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    d[i] = dr.get(i) + rstd * (d[i] - v[i] * dot - mean);
+                    d[i] = rstd * (d[i] - v[i] * dot - mean);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    d[i] = dr.get(i);
+                    d[i] = 0.f;
             }
-            RawRow<TYPE, NT> out;
-            if (p.d_residual) {
+            if constexpr (kHalves)
+                in.load_second(p, row, t);
+            if (p.d_r) {
+                in.dr.get(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    out.put(i, d[i]);
+                    d[i] += v[i];
+            }
+            RawRow<TYPE, WHOLE> out;
+            if (p.d_residual) {
+                out.put(d);
                 out.store(p.d_residual, row * p.ld_dres, p.cols, t);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 d[i] *= p.scale;
             float rstd = 1.f;
-            if (p.post || p.gate) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = xraw.get(i);
-            }
+            if (p.post || p.gate)
+                in.x.get(v);
             if (p.post) {
                 rstd = centre<NT>(v, p, inv_n, lds, turn, t);
 #pragma unroll
@@ -318,25 +398,18 @@ __global__ void __launch_bounds__(Worker<NT>::kThreads) norm_backward_kernel(Nor
                     v[i] *= rstd;
             }
             if (p.gate) {
-                float n[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    n[i] = d[i] * v[i];
-                if (p.post)
-                    times(n, 1.f, post);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s_gate[i] += n[i];
-                times(d, 1.f, gate);
+                for (int i = 0; i < 8; ++i) {
+                    s_gate[i] += d[i] * (p.post ? v[i] * post[i] : v[i]);
+                    d[i] *= gate[i];
+                }
             }
             if (p.post) {
                 float s[2] = {0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s_post[i] += d[i] * v[i];
-                times(d, 1.f, post);
-#pragma unroll
                 for (int i = 0; i < 8; ++i) {
+                    s_post[i] += d[i] * v[i];
+                    d[i] *= post[i];
                     s[0] += d[i] * v[i];
                     s[1] += d[i];
                 }
@@ -346,22 +419,20 @@ __global__ void __launch_bounds__(Worker<NT>::kThreads) norm_backward_kernel(Nor
                 for (int i = 0; i < 8; ++i)
                     d[i] = rstd * (d[i] - v[i] * dot - mean);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                out.put(i, d[i]);
+            out.put(d);
             out.store(p.d_x, row * p.ld_dx, p.cols, t);
         }
         if (p.gate) {
             if (p.units == 1)
-                store_gate<NT>(p, g, s_gate, t);
+                store_gate(p, g, s_gate, t);
             else        // then a worker has one unit
-                store_part<NT>(p, 2, worker, s_gate, t);
+                store_part(p, 2, worker, s_gate, t);
         }
     }
     if (p.post)
-        store_part<NT>(p, 0, worker, s_post, t);
+        store_part(p, 0, worker, s_post, t);
     if (p.pre)
-        store_part<NT>(p, 1, worker, s_pre, t);
+        store_part(p, 1, worker, s_pre, t);
 }
 
 // Column sums of the workers' partial rows: 64 columns a work-group, its
@@ -414,44 +485,53 @@ NormShape norm_shape(int cols)
     return {threads, threads};
 }
 
-template <int TYPE, int NT>
+template <int TYPE, int NT, bool WHOLE>
 static void norm_launch(const NormArgs& a, bool backward, int cus, hipStream_t stream)
 {
     typedef Worker<NT> W;
     if (backward) {
-        hipLaunchKernelGGL((norm_backward_kernel<TYPE, NT>),
+        hipLaunchKernelGGL((norm_backward_kernel<TYPE, NT, WHOLE>),
                            dim3((unsigned)((a.workers + W::kPerGroup - 1) / W::kPerGroup)), dim3(W::kThreads), 0, stream, a);
         return;
     }
     int64_t groups = (a.rows + W::kPerGroup - 1) / W::kPerGroup;
     const int64_t most = (int64_t)cus * (2048 / W::kThreads);       // as many as are resident
     groups = groups < most ? groups : most;
-    hipLaunchKernelGGL((norm_kernel<TYPE, NT>), dim3((unsigned)groups), dim3(W::kThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<TYPE, NT, WHOLE>), dim3((unsigned)groups), dim3(W::kThreads), 0, stream, a);
 }
 
-template <int TYPE>
+template <int TYPE, bool WHOLE>
 static void norm_launch(const NormArgs& a, bool backward, int cus, hipStream_t stream)
 {
     if (a.cols <= 512)
-        norm_launch<TYPE, 64>(a, backward, cus, stream);
+        norm_launch<TYPE, 64, WHOLE>(a, backward, cus, stream);
     else if (a.cols <= 1024)
-        norm_launch<TYPE, 128>(a, backward, cus, stream);
+        norm_launch<TYPE, 128, WHOLE>(a, backward, cus, stream);
     else if (a.cols <= 2048)
-        norm_launch<TYPE, 256>(a, backward, cus, stream);
+        norm_launch<TYPE, 256, WHOLE>(a, backward, cus, stream);
     else if (a.cols <= 4096)
-        norm_launch<TYPE, 512>(a, backward, cus, stream);
+        norm_launch<TYPE, 512, WHOLE>(a, backward, cus, stream);
     else
-        norm_launch<TYPE, 1024>(a, backward, cus, stream);
+        norm_launch<TYPE, 1024, WHOLE>(a, backward, cus, stream);
 }
 
 static hipError_t norm_any(const NormArgs& a, int type, bool backward, int cus, hipStream_t stream)
 {
-    if (type == kBF16)
-        norm_launch<kBF16>(a, backward, cus, stream);
-    else if (type == kFP16)
-        norm_launch<kFP16>(a, backward, cus, stream);
-    else
-        norm_launch<kFP32>(a, backward, cus, stream);
+    if (a.cols % 8 == 0) {
+        if (type == kBF16)
+            norm_launch<kBF16, true>(a, backward, cus, stream);
+        else if (type == kFP16)
+            norm_launch<kFP16, true>(a, backward, cus, stream);
+        else
+            norm_launch<kFP32, true>(a, backward, cus, stream);
+    } else {
+        if (type == kBF16)
+            norm_launch<kBF16, false>(a, backward, cus, stream);
+        else if (type == kFP16)
+            norm_launch<kFP16, false>(a, backward, cus, stream);
+        else
+            norm_launch<kFP32, false>(a, backward, cus, stream);
+    }
     return hipGetLastError();
 }
 
