@@ -4,6 +4,7 @@
 #include "block.h"
 #include "element.h"
 #include "quant.h"
+#include "schedule.h"
 #include "segments.h"
 #include "wave.h"
 
@@ -34,15 +35,15 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits)
 }
 
 // Codes of four elements, first in the low byte; round to nearest even.  (The
-// product of the block's largest element may come out a step over fmax.)
+// product of the block's largest element may come out an FP32 step over fmax,
+// which rounds to fmax.)
 template <int F>
 __device__ __forceinline__ uint32_t block_codes(const BlockScale& b, float x, float y, float z, float w)
 {
-    constexpr float kMax = F == kE5M2 ? 57344.f : 448.f;
-    x = __builtin_amdgcn_fmed3f(x * b.mul, -kMax, kMax);
-    y = __builtin_amdgcn_fmed3f(y * b.mul, -kMax, kMax);
-    z = __builtin_amdgcn_fmed3f(z * b.mul, -kMax, kMax);
-    w = __builtin_amdgcn_fmed3f(w * b.mul, -kMax, kMax);
+    x *= b.mul;
+    y *= b.mul;
+    z *= b.mul;
+    w *= b.mul;
     int c;
     if constexpr (F == kE5M2) {
         c = __builtin_amdgcn_cvt_pk_bf8_f32(x, y, 0, false);
@@ -144,6 +145,141 @@ __device__ __forceinline__ void put_columns(const TileLds& lds, uint8_t* out, in
 
 // ----------------------------------------------------------- activations ----
 
+// silu and its derivative a rounding or two from exact: a code hangs on which
+// side of a tie y lies, so errors of the shared, faster form (an exponential
+// that carries its argument's rounding) show as codes that differ: twice as
+// many from the exact ones' as this form has.  exp(-z) as 2^h (1 + l ln 2), h
+// and l the product -z log2 e in two parts; the reciprocal with one Newton step.
+__device__ __forceinline__ float sigmoid_near(float z)
+{
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147181f;
+    const float h = -z * kHi, l = fmaf(-z, kHi, -h) - z * kLo;
+    float e = __builtin_amdgcn_exp2f(h);
+    const float far = __builtin_amdgcn_rcpf(1.f + e);       // 0 or 1, or NaN
+    e = fmaf(e, l * kLn2, e);
+    const float d = 1.f + e, r = __builtin_amdgcn_rcpf(d);
+    return fabsf(h) < 126.f ? fmaf(fmaf(-d, r, 1.f), r, r) : far;
+}
+
+__device__ __forceinline__ void activate8(int act, float (&z)[8])
+{
+    if (act == kActSilu) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            z[u] *= sigmoid_near(z[u]);
+    } else {
+        activate(act, z);
+    }
+}
+
+// z becomes act'(z), y gets act(z)
+__device__ __forceinline__ void activate_grads8(int act, float (&z)[8], float (&y)[8])
+{
+    if (act == kActSilu) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float s = sigmoid_near(z[u]);
+            y[u] = z[u] * s;
+            z[u] = s * (1.f + z[u] * (1.f - s));
+        }
+    } else {
+        activate_grads(act, z, y);
+    }
+}
+
+// Eight elements as loaded.
+template <int TYPE>
+struct Raw {
+    uint32_t w[TYPE == kFP32 ? 8 : 4];
+    __device__ __forceinline__ void load(const void* base, int64_t at)
+    {
+        __builtin_memcpy(w, static_cast<const typename Element<TYPE>::T*>(base) + at, sizeof(w));
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if constexpr (TYPE == kFP32)
+                f[u] = __uint_as_float(w[u]);
+            else if constexpr (TYPE == kBF16)
+                f[u] = __uint_as_float(u & 1 ? w[u / 2] & 0xFFFF0000u : w[u / 2] << 16);
+            else
+                f[u] = Element<kFP16>::get((uint16_t)(w[u / 2] >> (16 * (u & 1))));
+        }
+    }
+};
+
+// The thread's eight rows of y from `row` on, columns c .. c + 7, where a row
+// comes in whole eights: the loads of kBatch rows go out before the first is
+// used.  Rows from `live` and columns from C on are zero; what is loaded there
+// is the last row, or the last eight columns, there is.
+template <int TYPE, bool BACK>
+__device__ __forceinline__ void values8x8(const BlockQuantArgs& p, int64_t row, int64_t live, int c, float (&v)[8][8])
+{
+    constexpr int kBatch = TYPE == kFP32 ? 2 : 4;
+    const int half = p.half;
+    const bool up = BACK && half && c >= half;
+    const int width = half ? half : p.C, at = up ? c - half : c;
+    const int cc = at < width ? at : width - 8;
+    const bool there = c < p.C;
+#pragma unroll
+    for (int i0 = 0; i0 < 8; i0 += kBatch) {
+        Raw<TYPE> x[kBatch], x1[BACK ? 1 : kBatch];
+        Raw<kBF16> z[BACK ? kBatch : 1], z1[BACK ? kBatch : 1];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            int64_t r = row + i0 + i;
+            r = r < live ? r : live > 0 ? live - 1 : 0;
+            x[i].load(p.x, r * p.ld_x + cc);
+            if constexpr (BACK) {
+                z[i].load(p.z, r * p.ld_z + cc);
+                if (half && !up)
+                    z1[i].load(p.z, r * p.ld_z + half + cc);
+            } else if (half) {
+                x1[i].load(p.x, r * p.ld_x + half + cc);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            float (&y)[8] = v[i0 + i];
+            x[i].get(y);
+            if constexpr (BACK) {
+                float s[8], a[8];
+                z[i].get(s);
+                activate_grads8(p.act, s, a);
+                if (up) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        y[u] *= a[u];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        y[u] *= s[u];
+                    if (half) {
+                        z1[i].get(a);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            y[u] *= a[u];
+                    }
+                }
+            } else {
+                activate8(p.act, y);
+                if (half) {
+                    float u1[8];
+                    x1[i].get(u1);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        y[u] *= u1[u];
+                }
+            }
+            const bool ok = there && row + i0 + i < live;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                y[u] = ok ? y[u] : 0.f;
+        }
+    }
+}
+
 // Eight columns of one row of y, from column c on (zero past C).
 template <int TYPE, bool BACK>
 __device__ __forceinline__ void value8(const BlockQuantArgs& p, int64_t row, int c, float (&v)[8])
@@ -152,12 +288,12 @@ __device__ __forceinline__ void value8(const BlockQuantArgs& p, int64_t row, int
     if constexpr (!BACK) {
         if (!half) {
             load8<TYPE>(p.x, row * p.ld_x, c, p.C, v);
-            activate(p.act, v);
+            activate8(p.act, v);
         } else {
             float u[8];
             load8<TYPE>(p.x, row * p.ld_x, c, half, v);
             load8<TYPE>(p.x, row * p.ld_x + half, c, half, u);
-            activate(p.act, v);
+            activate8(p.act, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] *= u[i];
@@ -173,7 +309,7 @@ __device__ __forceinline__ void value8(const BlockQuantArgs& p, int64_t row, int
             load8<kBF16>(p.z, row * p.ld_z, first, width, z);
             if (half && !up)
                 load8<kBF16>(p.z, row * p.ld_z + half, first, width, z1);
-            activate_grads(p.act, z, y);
+            activate_grads8(p.act, z, y);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] *= !half ? z[i] : up ? y[i] : z[i] * z1[i];
@@ -190,7 +326,7 @@ __device__ __forceinline__ void value8(const BlockQuantArgs& p, int64_t row, int
             load8<TYPE>(p.x, row * p.ld_x, col, col + 1, d);
             load8<kBF16>(p.z, row * p.ld_z, col, col + 1, z);
             load8<kBF16>(p.z, row * p.ld_z + half, col, col + 1, z1);
-            activate_grads(p.act, z, y);
+            activate_grads8(p.act, z, y);
             const float one = d[0] * (hi ? y[0] : z[0] * z1[0]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -232,11 +368,28 @@ __device__ __forceinline__ void clear_rest(const BlockQuantArgs& p, int chunk, i
     }
 }
 
-template <int F, int TYPE, bool BACK>
-__global__ void __launch_bounds__(256) block_quant_kernel(BlockQuantArgs p)
+// Gradient tiles of the two halves read the same columns of x and z, so a pair
+// of them goes to one XCD (whose work-groups are every eighth), one after the
+// other.
+__device__ __forceinline__ int paired_tile(const BlockQuantArgs& p)
+{
+    if (p.half == 0 || p.half % kTile != 0)
+        return blockIdx.x;
+    const int x = blockIdx.x, n = gridDim.x / 2;        // tiles of a half
+    const int whole = n / kNumXcd * kNumXcd, left = n - whole;
+    if (x < 2 * whole) {
+        const int i = x % (2 * kNumXcd);
+        return x / (2 * kNumXcd) * kNumXcd + i % kNumXcd + i / kNumXcd * n;
+    }
+    return whole + (x - 2 * whole) % left + (x - 2 * whole) / left * n;
+}
+
+// VEC: rows of whole eights.
+template <int F, int TYPE, bool BACK, bool VEC>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) block_quant_kernel(BlockQuantArgs p)
 {
     __shared__ TileLds lds;
-    const int tid = threadIdx.x, tc = blockIdx.x, chunk = blockIdx.y;
+    const int tid = threadIdx.x, tc = BACK && VEC ? paired_tile(p) : blockIdx.x, chunk = blockIdx.y;
     int row0 = chunk * kTile, end = p.rows, live = p.rows;
     if (!p.qt) {        // rows in any order: no segments, the dropped ones last
         if (p.offsets)
@@ -251,14 +404,18 @@ __global__ void __launch_bounds__(256) block_quant_kernel(BlockQuantArgs p)
     const int c = tc * kTile + 8 * (tid & 15);
     const int64_t row = row0 + 8 * (tid >> 4);
     float v[8][8];
+    if constexpr (VEC) {
+        values8x8<TYPE, BACK>(p, row, live, c, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (row + i < live) {
-            value8<TYPE, BACK>(p, row + i, c, v[i]);
-        } else {
+        for (int i = 0; i < 8; ++i) {
+            if (row + i < live) {
+                value8<TYPE, BACK>(p, row + i, c, v[i]);
+            } else {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                v[i][u] = 0.f;
+                for (int u = 0; u < 8; ++u)
+                    v[i][u] = 0.f;
+            }
         }
     }
     if (p.q)
@@ -337,10 +494,15 @@ template <int F, int TYPE>
 static void quant_launch(const BlockQuantArgs& a, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.C + kTile - 1) / kTile), (unsigned)a.chunks + (a.qt && a.offsets ? 1 : 0));
-    if (a.z)
-        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, true>), grid, dim3(256), 0, stream, a);
+    const bool vec = (a.half ? a.half : a.C) % 8 == 0;
+    if (a.z && vec)
+        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, true, true>), grid, dim3(256), 0, stream, a);
+    else if (a.z)
+        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, true, false>), grid, dim3(256), 0, stream, a);
+    else if (vec)
+        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, false, true>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, false>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((block_quant_kernel<F, TYPE, false, false>), grid, dim3(256), 0, stream, a);
 }
 
 template <int F>

@@ -44,6 +44,40 @@ def test_route(T, E, k, groups, top, bias, score, normalize, dtype):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top,bias", [(256, 8, 8, 4, True), (256, 8, 8, 4, False), (128, 6, 1, 1, False),
+                                                 (64, 4, 4, 2, True), (40, 8, 1, 1, True), (3, 2, 1, 1, False),
+                                                 (200, 16, 1, 1, True), (128, 8, 16, 3, True)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens_choose_as_few_do(E, k, groups, top, bias, score, dtype):
+    """The kernel for many tokens against the one for few (which the definition
+    checks), with keys that are equal, nearly equal, masked and tiny."""
+    torch_cuda()
+    g = torch.Generator().manual_seed(E + k)
+    T = 4096 + 37
+    x = _logits(g, T, E, torch.float32)
+    x[:300] = torch.round(x[:300])                      # ties
+    x[300:600] *= 30                                    # scores that end near 0 and 1
+    x[600:700, ::2] = -math.inf
+    x[700:720] = -math.inf
+    x[720:730, 1:] = math.nan
+    x[730:900] = x[730:900] * 1e-6                      # keys that differ by less than an FP32 step
+    x[900:1000] -= 90
+    x = x.to(dtype)
+    b = torch.randn(E, generator=g) * 0.2 if bias else None
+    if bias:
+        b[E // 3:E // 2] = 0.125
+    say(f"many tokens E={E} k={k} groups={groups}/{top} bias={bias} {score} {dtype}")
+    for normalize in (True, False):
+        how = dict(score=score, bias=None if b is None else b.cuda(), groups=groups, top_groups=top,
+                   normalize=normalize, scale=1.5)
+        ids, w = pkg.route_tokens(x.cuda(), k, **how)
+        few = [pkg.route_tokens(p, k, **how) for p in x.cuda().split(1500)]
+        assert torch.equal(ids, torch.cat([i for i, _ in few]))
+        ref = torch.cat([v for _, v in few]).double()
+        assert ((w.double() - ref).abs() <= 2 * bc.U * ref.abs()).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias,groups,top", [(False, 1, 1), (True, 1, 1), (True, 4, 2), (False, 4, 2)])
 def test_masked_and_unusual_logits(bias, groups, top, score):
     """Rows with few or no experts left, infinities, NaN, ties, far logits."""
