@@ -244,7 +244,7 @@ __device__ __forceinline__ void block_step(const uint8_t* a, const uint8_t* w, c
 // SIMD the other one's fill what is left.
 template <int GA, int GB, bool SQUARES, int FA, int FB, class Copies, class Src>
 __device__ __forceinline__ void native_block_loop(const Copies& co, const Src& src_at, uint8_t* lds, int nsteps, int wl,
-                                                  int a_row, int w_row, int lane, v16f (&acc)[GA][GB])
+                                                  int a_row, int w_row, bool idle, int lane, v16f (&acc)[GA][GB])
 {
     typedef typename Copies::G G;
     constexpr int kSlots = GA * GB * 2, kRow = GB * 2;      // MFMAs of a K-step, of 32 rows
@@ -267,6 +267,15 @@ __device__ __forceinline__ void native_block_loop(const Copies& co, const Src& s
     co.issue_all(src_at(last < 1 ? last : 1), lds, 1, wl);
     wait_copies<G::COPIES>();
     __syncthreads();
+    if (idle) {         // copies and barriers only; the SIMD's other wave has its matrix unit
+        for (int s = 0; s < nsteps; ++s) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            co.issue_all(src_at(s + 2 < last ? s + 2 : last), lds, s & 1, wl);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        return;
+    }
 #pragma unroll
     for (int g = 0; g < GB; ++g)
 #pragma unroll
@@ -396,6 +405,8 @@ block_linear_kernel(BlockLinArgs p)
         const int first = it.k0 + wk * share + (wk < more ? wk : more);
         uint8_t* const mem = lds + wk * G::BYTES;
         const float* const scales = reinterpret_cast<const float*>(mem + 2 * G::CODES);
+        // a wave whose rows (or columns) all lie past the edge multiplies nothing
+        const bool idle = it.m0 + wm * TM >= it.end || n0 + wn * TN >= p.N;
         Copies co;
         co.init(p, it.m0, it.end, n0, wl, lane);
         const BlockSrc src0 = {
@@ -409,23 +420,32 @@ block_linear_kernel(BlockLinArgs p)
                             src0.ws + s * p.ws_k * 4};
         };
         if constexpr (BM == 256) {
-            native_block_loop<GA, GB, SQUARES, FA, FB>(co, src_at, mem, nsteps, wl, wm * TM, wn * TN, lane, acc);
+            native_block_loop<GA, GB, SQUARES, FA, FB>(co, src_at, mem, nsteps, wl, wm * TM, wn * TN, idle, lane,
+                                                       acc);
         } else {
-        if (nsteps > 0)
-            co.issue_all(src_at(0), mem, 0, wl);
-        for (int s = 0; s < nsteps; ++s) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if constexpr (NWG > 1)
-                __syncthreads();        // step s has landed; step s - 1 is read
-            if (s + 1 < nsteps)
-                co.issue_all(src_at(s + 1), mem, (s + 1) & 1, wl);
-            const uint8_t* const codes = mem + (s & 1) * G::CODES;
-            const float* const sc = scales + (s & 1) * (BM + BN);
-            block_step<GA, GB, EXACT, SQUARES, FA, FB>(codes + wm * TM * kBK, codes + G::A_BYTES + wn * TN * kBK,
-                                                       sc + wm * TM, sc + BM + wn * TN, lane, acc);
-            if constexpr (NWG == 1)
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read before it is copied over
-        }
+            // the first two steps' copies go out together (short inner ranges wait
+            // for little else)
+            if (nsteps > 0)
+                co.issue_all(src_at(0), mem, 0, wl);
+            if (nsteps > 1)
+                co.issue_all(src_at(1), mem, 1, wl);
+            for (int s = 0; s < nsteps; ++s) {
+                if (s == 0 && nsteps > 1)
+                    wait_copies<G::COPIES>();
+                else
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                if constexpr (NWG > 1)
+                    __syncthreads();        // step s has landed; step s - 1 is read
+                if (s > 0 && s + 1 < nsteps)
+                    co.issue_all(src_at(s + 1), mem, (s + 1) & 1, wl);
+                const uint8_t* const codes = mem + (s & 1) * G::CODES;
+                const float* const sc = scales + (s & 1) * (BM + BN);
+                if (!idle)
+                    block_step<GA, GB, EXACT, SQUARES, FA, FB>(codes + wm * TM * kBK, codes + G::A_BYTES + wn * TN * kBK,
+                                                           sc + wm * TM, sc + BM + wn * TN, lane, acc);
+                if constexpr (NWG == 1)
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read before it is copied over
+            }
         }
     }
     __syncthreads();        // every wave has read its last fragments

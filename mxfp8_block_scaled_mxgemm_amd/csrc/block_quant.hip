@@ -4,17 +4,18 @@
 #include "block.h"
 #include "element.h"
 #include "quant.h"
-#include "schedule.h"
 #include "segments.h"
 #include "wave.h"
 
 namespace mxg {
 
 // A block's scale and what its elements are multiplied by.  The scale is the
-// largest magnitude over the format's, at least 2^-126 so that its reciprocal
-// is a number; a block that holds a NaN or an infinity has a NaN scale and NaN
-// codes, since no scale represents it.  The codes are rounded from y (fmax /
-// amax), one FP32 rounding of the factor and one of the product away from y / s.
+// largest magnitude over the format's (7 2^6 or 7 2^13: times 1 / 7, in two
+// parts), at least 2^-126 so that its reciprocal is a number; a block that holds
+// a NaN or an infinity has a NaN scale and NaN codes, since no scale represents
+// it.  The factor is the scale's reciprocal (one Newton step from the
+// hardware's); the codes are rounded from its FP32 product with y.  (Divisions
+// instead cost a fifth of all instructions.)
 struct BlockScale {
     float s, mul;
     bool nan;
@@ -23,14 +24,16 @@ struct BlockScale {
 template <int F>
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits)
 {
-    constexpr float kMax = F == kE5M2 ? 57344.f : 448.f;
+    constexpr float kUnit = F == kE5M2 ? 1.f / 8192 : 1.f / 64;
+    constexpr float kHi = 0.142857149f * kUnit, kLo = -6.386212e-09f * kUnit;      // 1 / 7
     constexpr float kLow = 1.1754943508222875e-38f;     // 2^-126
     const float amax = __uint_as_float(amax_bits);
     BlockScale b;
     b.nan = amax_bits >= 0x7F800000u;
-    const bool low = amax <= kMax * kLow;
-    b.s = b.nan ? __uint_as_float(0x7FC00000u) : low ? kLow : amax / kMax;
-    b.mul = low ? 8.507059173023462e37f : kMax / amax;  // 2^126
+    b.s = fmaxf(fmaf(amax, kHi, amax * kLo), kLow);
+    const float r = __builtin_amdgcn_rcpf(b.s);
+    b.mul = fmaf(fmaf(-b.s, r, 1.f), r, r);
+    b.s = b.nan ? __uint_as_float(0x7FC00000u) : b.s;
     return b;
 }
 
@@ -67,79 +70,86 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 // codes; the tile of those goes through LDS so that whole columns of 128 bytes
 // are written.
 constexpr int kTile = 128;
-constexpr int kTileRow = kTile + 16;        // bytes between columns in LDS: 16-byte pieces, spread over the banks
 
 struct TileLds {
     uint32_t amax[4][kTile];
-    uint8_t codes[kTile * kTileRow];
+    BlockScale scale[kTile];
+    uint8_t codes[kTile * kTile];
 };
 
-// Codes along the columns of the thread's rows [row0 + 8 r, ..) below `end`;
-// those from `live` on are zero, codes and scales.
-template <int F>
-__device__ __forceinline__ void put_rows8(const float (&v)[8][8], uint8_t* q, int64_t ld_q, float* s, int64_t ld_s,
-                                          int64_t row, int64_t end, int64_t live, int tc, int tid)
+// Byte of (column, row) in the tile of transposed codes: rows of 128 bytes whose
+// 16-byte chunks are swizzled, so that neither eight columns apart (the writes)
+// nor whole columns (the reads) meet in a few banks.
+__device__ __forceinline__ int code_at(int col, int row)
+{
+    return col * kTile + ((((row >> 4) ^ (col >> 3)) & 7) << 4) + (row & 15);
+}
+
+// Codes along the columns of N of a thread's rows [row, ..) below `end`, block tb
+// of the row; those from `live` on are zero, codes and scales.
+template <int F, int N>
+__device__ __forceinline__ void put_rows8(const float (&v)[N][8], uint8_t* q, int64_t ld_q, float* s, int64_t ld_s,
+                                          int64_t row, int64_t end, int64_t live, int tb, int tid)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
         uint32_t m = 0;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             m = max(m, magnitude(v[i][u]));
         const BlockScale b = block_scale<F>(row16_max(m));
         if (row + i < end) {
-            *reinterpret_cast<u32x2*>(q + (row + i) * ld_q + tc * kTile + 8 * (tid & 15)) =
+            *reinterpret_cast<u32x2*>(q + (row + i) * ld_q + tb * kTile + 8 * (tid & 15)) =
                 u32x2{block_codes<F>(b, v[i][0], v[i][1], v[i][2], v[i][3]),
                       block_codes<F>(b, v[i][4], v[i][5], v[i][6], v[i][7])};
             if ((tid & 15) == 0)
-                s[tc * ld_s + row + i] = row + i < live ? b.s : 0.f;
+                s[tb * ld_s + row + i] = row + i < live ? b.s : 0.f;
         }
     }
 }
 
-// The eight columns' maxima over the tile's 128 rows.
-__device__ __forceinline__ void column_max(const float (&v)[8][8], TileLds& lds, uint32_t (&m)[8], int tid)
+// The eight columns' maxima over the wave's rows, for lds.amax.
+template <int N>
+__device__ __forceinline__ void column_max(const float (&v)[N][8], uint32_t* amax, int lane)
 {
-    const int lane = tid & 63, wave = tid >> 6;
+    uint32_t m[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         m[u] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             m[u] = max(m[u], magnitude(v[i][u]));
         m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 16));
         m[u] = max(m[u], (uint32_t)__shfl_xor((int)m[u], 32));
     }
-    if (lane < 16)
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            lds.amax[wave][8 * lane + u] = m[u];
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int c = 8 * (tid & 15) + u;
-        m[u] = max(max(lds.amax[0][c], lds.amax[1][c]), max(lds.amax[2][c], lds.amax[3][c]));
+    if (lane < 16) {
+        *reinterpret_cast<u32x4*>(amax + 8 * lane) = u32x4{m[0], m[1], m[2], m[3]};
+        *reinterpret_cast<u32x4*>(amax + 8 * lane + 4) = u32x4{m[4], m[5], m[6], m[7]};
     }
 }
 
-template <int F>
-__device__ __forceinline__ void flip(const float (&v)[8][8], const BlockScale& b, int u, TileLds& lds, int tid)
+// N rows of the thread's column u, transposed, to the tile of codes.
+template <int F, int N>
+__device__ __forceinline__ void flip(const float (&v)[N][8], const BlockScale& b, int u, uint8_t* codes, int row, int tid)
 {
-    *reinterpret_cast<u32x2*>(lds.codes + (8 * (tid & 15) + u) * kTileRow + 8 * (tid >> 4)) =
-        u32x2{block_codes<F>(b, v[0][u], v[1][u], v[2][u], v[3][u]),
-              block_codes<F>(b, v[4][u], v[5][u], v[6][u], v[7][u])};
+    uint8_t* to = codes + code_at(8 * (tid & 15) + u, row);
+    if constexpr (N == 8)
+        *reinterpret_cast<u32x2*>(to) = u32x2{block_codes<F>(b, v[0][u], v[1][u], v[2][u], v[3][u]),
+                                              block_codes<F>(b, v[4][u], v[5][u], v[6][u], v[7][u])};
+    else
+        *reinterpret_cast<uint32_t*>(to) = block_codes<F>(b, v[0][u], v[1][u], v[2][u], v[3][u]);
 }
 
 // The transposed codes out of LDS: column c of the tile, below `cols`, to row
-// c of out.
-__device__ __forceinline__ void put_columns(const TileLds& lds, uint8_t* out, int64_t ld, int cols, int tid)
+// c of out, by NT threads.
+template <int NT>
+__device__ __forceinline__ void put_columns(const uint8_t* codes, uint8_t* out, int64_t ld, int cols, int tid)
 {
-    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int c = 32 * k + (tid >> 3), at = 16 * (tid & 7);
+    for (int k = 0; k < kTile * 8 / NT; ++k) {
+        const int c = NT / 8 * k + (tid >> 3), at = 16 * (tid & 7);
         if (c < cols)
-            *reinterpret_cast<u32x4*>(out + c * ld + at) = *reinterpret_cast<const u32x4*>(lds.codes + c * kTileRow + at);
+            *reinterpret_cast<u32x4*>(out + c * ld + at) = *reinterpret_cast<const u32x4*>(codes + code_at(c, at));
     }
 }
 
@@ -216,7 +226,7 @@ struct Raw {
 template <int TYPE, bool BACK>
 __device__ __forceinline__ void values8x8(const BlockQuantArgs& p, int64_t row, int64_t live, int c, float (&v)[8][8])
 {
-    constexpr int kBatch = TYPE == kFP32 ? 2 : 4;
+    constexpr int kBatch = TYPE == kFP32 || BACK ? 2 : 4;
     const int half = p.half;
     const bool up = BACK && half && c >= half;
     const int width = half ? half : p.C, at = up ? c - half : c;
@@ -368,28 +378,12 @@ __device__ __forceinline__ void clear_rest(const BlockQuantArgs& p, int chunk, i
     }
 }
 
-// Gradient tiles of the two halves read the same columns of x and z, so a pair
-// of them goes to one XCD (whose work-groups are every eighth), one after the
-// other.
-__device__ __forceinline__ int paired_tile(const BlockQuantArgs& p)
-{
-    if (p.half == 0 || p.half % kTile != 0)
-        return blockIdx.x;
-    const int x = blockIdx.x, n = gridDim.x / 2;        // tiles of a half
-    const int whole = n / kNumXcd * kNumXcd, left = n - whole;
-    if (x < 2 * whole) {
-        const int i = x % (2 * kNumXcd);
-        return x / (2 * kNumXcd) * kNumXcd + i % kNumXcd + i / kNumXcd * n;
-    }
-    return whole + (x - 2 * whole) % left + (x - 2 * whole) / left * n;
-}
-
 // VEC: rows of whole eights.
 template <int F, int TYPE, bool BACK, bool VEC>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) block_quant_kernel(BlockQuantArgs p)
 {
     __shared__ TileLds lds;
-    const int tid = threadIdx.x, tc = BACK && VEC ? paired_tile(p) : blockIdx.x, chunk = blockIdx.y;
+    const int tid = threadIdx.x, tc = blockIdx.x, chunk = blockIdx.y;
     int row0 = chunk * kTile, end = p.rows, live = p.rows;
     if (!p.qt) {        // rows in any order: no segments, the dropped ones last
         if (p.offsets)
@@ -422,17 +416,113 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) b
         put_rows8<F>(v, p.q, (int64_t)(p.C + kTile - 1) / kTile * kTile, p.s, p.rows, row, end, live, tc, tid);
     if (!p.qt)
         return;
-    uint32_t m[8];
-    column_max(v, lds, m, tid);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const BlockScale b = block_scale<F>(m[u]);
-        flip<F>(v, b, u, lds, tid);
-        if (tid < 16 && c + u < p.C)
-            p.st[(int64_t)chunk * p.C + c + u] = b.s;
+    column_max(v, lds.amax[tid >> 6], tid & 63);
+    __syncthreads();
+    if (tid < kTile) {
+        const BlockScale b = block_scale<F>(max(max(lds.amax[0][tid], lds.amax[1][tid]),
+                                                max(lds.amax[2][tid], lds.amax[3][tid])));
+        lds.scale[tid] = b;
+        if (tc * kTile + tid < p.C)
+            p.st[(int64_t)chunk * p.C + tc * kTile + tid] = b.s;
     }
-    const int cols = p.C - tc * kTile;
-    put_columns(lds, p.qt + (int64_t)tc * kTile * p.ld_qt + (int64_t)chunk * kTile, p.ld_qt, cols, tid);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        flip<F>(v, lds.scale[8 * (tid & 15) + u], u, lds.codes, 8 * (tid >> 4), tid);
+    __syncthreads();
+    put_columns<256>(lds.codes, p.qt + (int64_t)tc * kTile * p.ld_qt + (int64_t)chunk * kTile, p.ld_qt, p.C - tc * kTile,
+                     tid);
+}
+
+// A gated gradient whose halves are whole blocks: a work-group of 512 threads
+// takes the tile's columns of both halves, [x u act'(g), x act(g)], so that x, g
+// and u are read and the activation is evaluated once; a thread has four rows.
+struct PairLds {
+    uint32_t amax[2][8][kTile];
+    BlockScale scale[2][kTile];
+    uint8_t codes[2][kTile * kTile];
+};
+
+template <int F, int TYPE>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(TYPE == kFP32 ? 2 : 4)))
+block_quant_pair_kernel(BlockQuantArgs p)
+{
+    __shared__ PairLds lds;
+    const int tid = threadIdx.x, tc = blockIdx.x, chunk = blockIdx.y, tiles = p.half / kTile;
+    int row0 = chunk * kTile, end = p.rows, live = p.rows;
+    if (!p.qt) {        // rows in any order: no segments, the dropped ones last
+        if (p.offsets)
+            live = min(max(p.offsets[p.groups], 0), p.rows);
+    } else {
+        if (!segment_rows(p, chunk, row0, end)) {
+            if (tid < 256) {
+                clear_rest(p, chunk, tc);
+                clear_rest(p, chunk, tc + tiles);
+            }
+            return;
+        }
+        live = end;
+    }
+    const int c = tc * kTile + 8 * (tid & 15);
+    const int64_t row = row0 + 4 * (tid >> 4);
+    float v[4][8], w[4][8];
+    constexpr int kBatch = TYPE == kFP32 ? 1 : 2;       // rows whose loads go out together
+#pragma unroll
+    for (int i0 = 0; i0 < 4; i0 += kBatch) {
+        Raw<TYPE> x[kBatch];
+        Raw<kBF16> g[kBatch], u[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            int64_t r = row + i0 + i;
+            r = r < live ? r : live > 0 ? live - 1 : 0;
+            x[i].load(p.x, r * p.ld_x + c);
+            g[i].load(p.z, r * p.ld_z + c);
+            u[i].load(p.z, r * p.ld_z + p.half + c);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            float d[8], s[8], a[8], y[8];
+            x[i].get(d);
+            g[i].get(s);
+            u[i].get(y);
+            activate_grads8(p.act, s, a);
+            const bool ok = row + i0 + i < live;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[i0 + i][k] = ok ? d[k] * s[k] * y[k] : 0.f;
+                w[i0 + i][k] = ok ? d[k] * a[k] : 0.f;
+            }
+        }
+    }
+    if (p.q) {
+        put_rows8<F>(v, p.q, p.C, p.s, p.rows, row, end, live, tc, tid);
+        put_rows8<F>(w, p.q, p.C, p.s, p.rows, row, end, live, tc + tiles, tid);
+    }
+    if (!p.qt)
+        return;
+    column_max(v, lds.amax[0][tid >> 6], tid & 63);
+    column_max(w, lds.amax[1][tid >> 6], tid & 63);
+    __syncthreads();
+    if (tid < 2 * kTile) {
+        const int h = tid / kTile, k = tid % kTile;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = max(m, lds.amax[h][i][k]);
+        const BlockScale b = block_scale<F>(m);
+        lds.scale[h][k] = b;
+        p.st[(int64_t)chunk * p.C + h * p.half + tc * kTile + k] = b.s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        flip<F>(v, lds.scale[0][8 * (tid & 15) + k], k, lds.codes[0], 4 * (tid >> 4), tid);
+        flip<F>(w, lds.scale[1][8 * (tid & 15) + k], k, lds.codes[1], 4 * (tid >> 4), tid);
+    }
+    __syncthreads();
+    uint8_t* const out = p.qt + (int64_t)tc * kTile * p.ld_qt + (int64_t)chunk * kTile;
+    put_columns<512>(lds.codes[0], out, p.ld_qt, kTile, tid);
+    put_columns<512>(lds.codes[1], out + p.half * p.ld_qt, p.ld_qt, kTile, tid);
 }
 
 // ---------------------------------------------------------------- squares ----
@@ -483,9 +573,11 @@ __global__ void __launch_bounds__(256) square_quant_kernel(SquareQuantArgs p)
         return;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-        flip<F>(v, b, u, lds, tid);
+        flip<F>(v, b, u, lds.codes, 8 * (tid >> 4), tid);
+    __syncthreads();
     const int64_t ld = (int64_t)nb * kTile;
-    put_columns(lds, p.qt + (e * p.K + (int64_t)tk * kTile) * ld + (int64_t)tn * kTile, ld, p.K - tk * kTile, tid);
+    put_columns<256>(lds.codes, p.qt + (e * p.K + (int64_t)tk * kTile) * ld + (int64_t)tn * kTile, ld, p.K - tk * kTile,
+                     tid);
 }
 
 // ----------------------------------------------------------------- launch --
@@ -495,7 +587,9 @@ static void quant_launch(const BlockQuantArgs& a, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.C + kTile - 1) / kTile), (unsigned)a.chunks + (a.qt && a.offsets ? 1 : 0));
     const bool vec = (a.half ? a.half : a.C) % 8 == 0;
-    if (a.z && vec)
+    if (a.z && a.half && a.half % kTile == 0)
+        hipLaunchKernelGGL((block_quant_pair_kernel<F, TYPE>), dim3(a.half / kTile, grid.y), dim3(512), 0, stream, a);
+    else if (a.z && vec)
         hipLaunchKernelGGL((block_quant_kernel<F, TYPE, true, true>), grid, dim3(256), 0, stream, a);
     else if (a.z)
         hipLaunchKernelGGL((block_quant_kernel<F, TYPE, true, false>), grid, dim3(256), 0, stream, a);
