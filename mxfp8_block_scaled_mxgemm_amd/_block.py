@@ -75,6 +75,11 @@ def _pick(table, name, what):
         raise ValueError(f"unknown {what} {name!r}: one of {', '.join(table)}") from None
 
 
+def _new(shape, dtype, device):
+    """A contiguous matrix (the quickest of torch's ways to one)."""
+    return _moe.torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+
+
 def _matrix(t, name, device=None, dtypes=None, shape=None):
     ld = _rows_of(t, name, device, dtypes, shape)
     if t.dim() != 2:
@@ -107,11 +112,9 @@ def route_tokens(logits, k: int, score="softmax", bias=None, groups: int = 1, to
             k > E // groups * top_groups:
         raise ValueError(f"cannot choose {k} of {E} experts in {top_groups} of {groups} groups (at most 64 choices, "
                          "1024 experts, 64 groups)")
-    mem = torch.empty((2, T, k), dtype=torch.int32, device=dev)
-    ids, weights = mem[0], mem[1].view(torch.float32)
-    p = mem.data_ptr()
+    ids, weights = _new((T, k), torch.int32, dev), _new((T, k), torch.float32, dev)
     _run(_load().mxgemm_route_tokens, dev, logits.data_ptr(), ld, _TYPES[logits.dtype], T, E, k, kind, b, groups,
-         top_groups, 1 if normalize else 0, scale, p, p + 4 * T * k)
+         top_groups, 1 if normalize else 0, scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -128,7 +131,7 @@ def route_tokens_backward(d_weights, logits, ids, score="softmax", normalize=Tru
     k = ids.shape[1]
     if not 1 <= k <= min(64, E) or E > 1024:
         raise ValueError(f"{k} choices of {E} experts (at most 64 of 1024)")
-    out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    out = _new((T, E), logits.dtype, dev)
     _run(_load().mxgemm_route_tokens_backward, dev, _plain(d_weights, "d_weights", dev, torch.float32, (T, k)),
          logits.data_ptr(), ld, _TYPES[logits.dtype], T, E, k, _pick(SCORES, score, "score"), 1 if normalize else 0,
          scale, _plain(ids, "ids", dev, torch.int32, (T, k)), out.data_ptr(), E)
@@ -160,11 +163,9 @@ def _quantize(x, z, act, gated, sort, fmt, rows, cols):
     fmt, act = _format(fmt), _activation(act)
     q = s = qt = st = None
     if rows:
-        q = torch.empty((M, Cp), dtype=torch.uint8, device=dev)
-        s = torch.empty((Cp // STEP, M), dtype=torch.float32, device=dev)
+        q, s = _new((M, Cp), torch.uint8, dev), _new((Cp // STEP, M), torch.float32, dev)
     if cols:
-        qt = torch.empty((C, ld_qt), dtype=torch.uint8, device=dev)
-        st = torch.empty((ld_qt // STEP, C), dtype=torch.float32, device=dev)
+        qt, st = _new((C, ld_qt), torch.uint8, dev), _new((ld_qt // STEP, C), torch.float32, dev)
     _run(_load().mxgemm_block_quantize, dev, x.data_ptr(), _TYPES[x.dtype], ld_x,
          None if z is None else z.data_ptr(), ld_z, M, C, act, 1 if gated else 0, off or None, koff or None, E, fmt,
          None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
@@ -271,9 +272,11 @@ def _linear(a, a_scale, w, w_scale, offsets, mode, out_dtype, precision, a_fmt, 
             raise ValueError("no experts")
     if out_dtype not in _TYPES:
         raise ValueError(f"out_dtype {out_dtype!r} is not a 16- or 32-bit float type")
-    out = torch.empty((E, M, N) if mode == GROUP_INNER else (M, N), dtype=out_dtype, device=dev)
-    work_ptr = 0
-    work = _split_workspace(M, N, K) if mode == GROUP_NONE else 0
+    out = torch.empty((E, M, N), dtype=out_dtype, device=dev) if mode == GROUP_INNER else _new((M, N), out_dtype, dev)
+    work_ptr = work = 0
+    # (few rows of squares are not split: block.cpp's choose_tile)
+    if mode == GROUP_NONE and not (squares and M <= 64 and -(-M // 32) * -(-N // 16) <= 256 and tile_cfg < 0):
+        work = _split_workspace(M, N, K)
     if work:
         work_mem = torch.empty(work, dtype=torch.uint8, device=dev)
         work_ptr = work_mem.data_ptr()
@@ -379,7 +382,6 @@ def add_norm(x, residual=None, gate=None, scale: float = 1.0, post_weight=None, 
     T / G rows (each sequence its own; G = T: each token); weights [H]; gate and
     weights may be of any of the types.  kind: "rms" or "layer" (mean taken
     off)."""
-    torch = _moe.torch
     ld_x = _matrix(x, "x", dtypes=_TYPES)
     dev = x.device
     T, H = x.shape
@@ -392,8 +394,8 @@ def add_norm(x, residual=None, gate=None, scale: float = 1.0, post_weight=None, 
     g_ptr, ld_g, G, g_type = _gate(gate, T, H, dev)
     post, post_type = _weight(post_weight, "post_weight", dev, H)
     pre, pre_type = _weight(pre_weight, "pre_weight", dev, H)
-    r = torch.empty((T, H), dtype=x.dtype, device=dev)
-    y = None if pre_weight is None else torch.empty((T, H), dtype=x.dtype, device=dev)
+    r = _new((T, H), x.dtype, dev)
+    y = None if pre_weight is None else _new((T, H), x.dtype, dev)
     _run(_load().mxgemm_add_norm, dev, NORM_ARGS.pack(
         x.data_ptr(), res_ptr, g_ptr, post, pre, r.data_ptr(), 0 if y is None else y.data_ptr(), 0, 0, 0, 0, 0, 0, 0,
         0, 0, T, H, G, ld_x, ld_res, ld_g, H, H, 0, 0, 0, 0, _TYPES[x.dtype], g_type, post_type, pre_type,
@@ -424,10 +426,10 @@ def add_norm_backward(d_y, d_r, x, r, gate=None, scale: float = 1.0, post_weight
     g_ptr, ld_g, G, g_type = _gate(gate, T, H, dev)
     post, post_type = _weight(post_weight, "post_weight", dev, H)
     pre, pre_type = _weight(pre_weight, "pre_weight", dev, H)
-    d_x = torch.empty((T, H), dtype=x.dtype, device=dev)
-    d_res = torch.empty((T, H), dtype=x.dtype, device=dev) if residual else None
+    d_x = _new((T, H), x.dtype, dev)
+    d_res = _new((T, H), x.dtype, dev) if residual else None
     d_gate = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-    sums = torch.empty((2, H), dtype=torch.float32, device=dev)
+    sums = _new((2, H), torch.float32, dev)
     lib = _load()
     size = lib.mxgemm_add_norm_workspace(T, H, G)
     work = torch.empty(size, dtype=torch.uint8, device=dev)
