@@ -62,9 +62,9 @@ int mxgemm_route_tokens_backward(const float* d_weights, const void* logits, int
 /* --------------------------------------------------------------- quantise --
  * FP8 codes (MXGEMM_FMT_*) with a float32 scale for each block of 128:
  *   s = max(amax / fmax, 2^-126),  q = y / s rounded to nearest even
- * (fmax 448 or 57344; the factor 1 / s is rounded to float32 once).  A block
- * that holds a NaN or an infinity has scale NaN and codes 0x7F.  Quantised is,
- * in FP32,
+ * (fmax 448 or 57344; q from the quotient with s before its rounding, itself
+ * rounded to float32).  A block that holds a NaN or an infinity has scale NaN
+ * and codes 0x7F.  Quantised is, in FP32,
  *   z NULL: y = act(x), or, gated, act(x[:, :C]) * x[:, C:] with x [rows][2 C]
  *   else:   y = x act'(z), or, gated, [x u act'(g), x act(g)] with [g, u] = z
  *           (z bfloat16 [rows][C]; x [rows][C], gated [rows][C / 2])
@@ -153,9 +153,8 @@ int mxgemm_block_linear(const mxgemm_block_linear_t* args, void* stream);
  * in FP32; r is rounded to its type first, and y is of the rounded r.  x,
  * residual, r, y [rows][cols] of `type`, row strides in elements, any
  * alignment of the element type.  gate [gate_rows][cols] of gate_type: row i
- * for rows [i, i + 1) rows / gate_rows; gate_rows divides rows; its row stride may
- * be 0.  Weights
- * [cols] of their types.  1 <= cols <= 8192.
+ * for rows [i, i + 1) rows / gate_rows; gate_rows divides rows; its row stride
+ * may be 0.  Weights [cols] of their types.  1 <= cols <= 8192.
  *
  * Gradient, from d_y and d_r (either may be NULL: zero), x, and r as it was
  * written: d_x and d_residual (or NULL) of `type`, d_gate [gate_rows][cols] of

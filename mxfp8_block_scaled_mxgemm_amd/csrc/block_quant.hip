@@ -13,40 +13,44 @@ namespace mxg {
 // largest magnitude over the format's (7 2^6 or 7 2^13: times 1 / 7, in two
 // parts), at least 2^-126 so that its reciprocal is a number; a block that holds
 // a NaN or an infinity has a NaN scale and NaN codes, since no scale represents
-// it.  The factor is the scale's reciprocal (one Newton step from the
-// hardware's); the codes are rounded from its FP32 product with y.  (Divisions
-// instead cost a fifth of all instructions.)
+// it.  The factor is the reciprocal of the scale before its rounding, in two
+// parts, from the hardware's estimate and one Newton step: a code hangs on which
+// side of a tie the quotient lies, and so only the quotient's own rounding
+// counts.  (Divisions instead cost a fifth of all instructions.)
 struct BlockScale {
-    float s, mul;
-    bool nan;
+    float s, mul, low;      // NaN, all three, for a block of NaN codes
 };
 
 template <int F>
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits)
 {
     constexpr float kUnit = F == kE5M2 ? 1.f / 8192 : 1.f / 64;
-    constexpr float kHi = 0.142857149f * kUnit, kLo = -6.386212e-09f * kUnit;      // 1 / 7
+    constexpr float kHi = 0.142857149f * kUnit, kLo = -6.386212e-09f * kUnit;       // 1 / 7
     constexpr float kLow = 1.1754943508222875e-38f;     // 2^-126
     const float amax = __uint_as_float(amax_bits);
     BlockScale b;
-    b.nan = amax_bits >= 0x7F800000u;
-    b.s = fmaxf(fmaf(amax, kHi, amax * kLo), kLow);
-    const float r = __builtin_amdgcn_rcpf(b.s);
-    b.mul = fmaf(fmaf(-b.s, r, 1.f), r, r);
-    b.s = b.nan ? __uint_as_float(0x7FC00000u) : b.s;
+    b.s = fmaf(amax, kHi, amax * kLo);
+    float rest = fmaf(amax, kHi, -b.s) + amax * kLo;    // what the rounding of s left
+    rest = b.s < kLow ? 0.f : rest;
+    b.s = fmaxf(b.s, kLow);
+    const float r = __builtin_amdgcn_rcpf(b.s), e = fmaf(-b.s, r, 1.f) - rest * r;
+    b.mul = fmaf(e, r, r);
+    b.low = fmaf(e, r, r - b.mul);
+    if (amax_bits >= 0x7F800000u)
+        b.s = b.mul = b.low = __uint_as_float(0x7FC00000u);
     return b;
 }
 
 // Codes of four elements, first in the low byte; round to nearest even.  (The
-// product of the block's largest element may come out an FP32 step over fmax,
+// quotient of the block's largest element may come out an FP32 step over fmax,
 // which rounds to fmax.)
 template <int F>
 __device__ __forceinline__ uint32_t block_codes(const BlockScale& b, float x, float y, float z, float w)
 {
-    x *= b.mul;
-    y *= b.mul;
-    z *= b.mul;
-    w *= b.mul;
+    x = fmaf(x, b.mul, x * b.low);
+    y = fmaf(y, b.mul, y * b.low);
+    z = fmaf(z, b.mul, z * b.low);
+    w = fmaf(w, b.mul, w * b.low);
     int c;
     if constexpr (F == kE5M2) {
         c = __builtin_amdgcn_cvt_pk_bf8_f32(x, y, 0, false);
@@ -55,7 +59,7 @@ __device__ __forceinline__ uint32_t block_codes(const BlockScale& b, float x, fl
         c = __builtin_amdgcn_cvt_pk_fp8_f32(x, y, 0, false);
         c = __builtin_amdgcn_cvt_pk_fp8_f32(z, w, c, true);
     }
-    return b.nan ? 0x7F7F7F7Fu : (uint32_t)c;
+    return isnan(b.mul) ? 0x7F7F7F7Fu : (uint32_t)c;
 }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -73,7 +77,7 @@ constexpr int kTile = 128;
 
 struct TileLds {
     uint32_t amax[4][kTile];
-    BlockScale scale[kTile];
+    float2 factor[kTile + kTile / 8];
     uint8_t codes[kTile * kTile];
 };
 
@@ -126,6 +130,15 @@ __device__ __forceinline__ void column_max(const float (&v)[N][8], uint32_t* ama
         *reinterpret_cast<u32x4*>(amax + 8 * lane) = u32x4{m[0], m[1], m[2], m[3]};
         *reinterpret_cast<u32x4*>(amax + 8 * lane + 4) = u32x4{m[4], m[5], m[6], m[7]};
     }
+}
+
+// The factor of the thread's column u.  (One in nine places is empty: the
+// sixteen threads of a row read eight columns apart, of which all would meet in
+// an eighth of the banks.)
+__device__ __forceinline__ BlockScale factor_of(const float2* factor, int u, int tid)
+{
+    const float2 f = factor[9 * (tid & 15) + u];
+    return {0.f, f.x, f.y};
 }
 
 // N rows of the thread's column u, transposed, to the tile of codes.
@@ -421,14 +434,14 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) b
     if (tid < kTile) {
         const BlockScale b = block_scale<F>(max(max(lds.amax[0][tid], lds.amax[1][tid]),
                                                 max(lds.amax[2][tid], lds.amax[3][tid])));
-        lds.scale[tid] = b;
+        lds.factor[tid + tid / 8] = make_float2(b.mul, b.low);
         if (tc * kTile + tid < p.C)
             p.st[(int64_t)chunk * p.C + tc * kTile + tid] = b.s;
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-        flip<F>(v, lds.scale[8 * (tid & 15) + u], u, lds.codes, 8 * (tid >> 4), tid);
+        flip<F>(v, factor_of(lds.factor, u, tid), u, lds.codes, 8 * (tid >> 4), tid);
     __syncthreads();
     put_columns<256>(lds.codes, p.qt + (int64_t)tc * kTile * p.ld_qt + (int64_t)chunk * kTile, p.ld_qt, p.C - tc * kTile,
                      tid);
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) b
 // and u are read and the activation is evaluated once; a thread has four rows.
 struct PairLds {
     uint32_t amax[2][8][kTile];
-    BlockScale scale[2][kTile];
+    float2 factor[2][kTile + kTile / 8];
     uint8_t codes[2][kTile * kTile];
 };
 
@@ -510,14 +523,14 @@ block_quant_pair_kernel(BlockQuantArgs p)
         for (int i = 0; i < 8; ++i)
             m = max(m, lds.amax[h][i][k]);
         const BlockScale b = block_scale<F>(m);
-        lds.scale[h][k] = b;
+        lds.factor[h][k + k / 8] = make_float2(b.mul, b.low);
         p.st[(int64_t)chunk * p.C + h * p.half + tc * kTile + k] = b.s;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        flip<F>(v, lds.scale[0][8 * (tid & 15) + k], k, lds.codes[0], 4 * (tid >> 4), tid);
-        flip<F>(w, lds.scale[1][8 * (tid & 15) + k], k, lds.codes[1], 4 * (tid >> 4), tid);
+        flip<F>(v, factor_of(lds.factor[0], k, tid), k, lds.codes[0], 4 * (tid >> 4), tid);
+        flip<F>(w, factor_of(lds.factor[1], k, tid), k, lds.codes[1], 4 * (tid >> 4), tid);
     }
     __syncthreads();
     uint8_t* const out = p.qt + (int64_t)tc * kTile * p.ld_qt + (int64_t)chunk * kTile;
