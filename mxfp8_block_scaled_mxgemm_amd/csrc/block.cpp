@@ -242,7 +242,7 @@ int plan_linear(mxg::BlockLinArgs* a, int cfg, int cus, int64_t workspace_bytes)
 // no more).  The workers' partial rows are the workspace.
 void plan_norm(mxg::NormArgs* a, int64_t gate_rows)
 {
-    const int64_t most = 256 * 16 * 64 / mxg::norm_shape(a->cols).threads;
+    const int64_t most = 256 * 16 * 64 / mxg::norm_threads(a->cols);
     a->gates = gate_rows;
     a->per_gate = a->rows / gate_rows;
     a->units = 1;

@@ -40,11 +40,7 @@ struct NormArgs {
     float* part;                  // [3][workers][cols]: post, pre, gate
 };
 
-// Threads of a row and of a work-group.
-struct NormShape {
-    int threads, group;
-};
-NormShape norm_shape(int cols);
+int norm_threads(int cols);       // of a row: eight elements each
 hipError_t launch_norm(const NormArgs& a, int type, int cus, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs& a, int type, hipStream_t stream);
 

@@ -251,7 +251,12 @@ __device__ __forceinline__ void block_step(const uint8_t* a, const uint8_t* w, c
 // registers, and step s + 1 has landed), the first fragments and the scales of
 // step s + 1 and the copies of step s + 2.  So neither the barrier nor an LDS
 // read's latency stands between two MFMAs of a wave, and with two waves per
-// SIMD the other one's fill what is left.
+// SIMD the other one's fill what is left.  8192 x 8192 x 8192: 466 us (2.36
+// PFLOP/s), against 521 for a loop that reads, multiplies and adds in turn.  A
+// wave whose MFMA is due goes before the other's multiply-adds (without the
+// priority 478); a copy to a slot, since two held up its LDS reads (474).  The
+// matrix unit is busy 62% of the time at the clock it then runs at; without the
+// copies the loop takes 419, without the multiply-adds 430.
 template <int GA, int GB, bool SQUARES, int FA, int FB, class Copies, class Src>
 __device__ __forceinline__ void native_block_loop(const Copies& co, const Src& src_at, uint8_t* lds, int nsteps, int wl,
                                                   int a_row, int w_row, bool idle, int lane, v16f (&acc)[GA][GB])
@@ -457,6 +462,13 @@ __device__ __forceinline__ void block_epilogue(const BlockLinArgs& p, uint8_t* m
 // stages: while a K-step is multiplied, the next one's copies are on their
 // way.  A K group is a run of the K-steps with stages of its own; one of a
 // single wave reads only what it copied itself and needs no barrier.
+//
+// Tiles of 128 x 128 keep the simple loop: two work-groups on a compute unit fill
+// each other's waits (8192 x 8192 x 8192 native 562 us, 572 with the loop above;
+// exact 935, 1.18 PFLOP/s, where a plain BF16 product reaches 1.25).  Neither more
+// stages with one work-group (256 x 128 in three, 592; 128 x 128 in four, 959) nor
+// fragments read a step ahead there (909) do as well, and for 512 x 4096 x 4096,
+// whose 128 work-groups are alone, those took 32 us and this loop 26.
 template <int BM, int BN, int WGM, int WGN, int WGK, int WGS, bool EXACT, bool SQUARES, int FA, int FB>
 __global__ void __launch_bounds__(WGM * WGN * WGK * 64)
     __attribute__((amdgpu_waves_per_eu(WGM * WGN * WGK * WGS / 4, WGM * WGN * WGK * WGS / 4)))
@@ -568,7 +580,11 @@ block_linear_kernel(BlockLinArgs p)
 // +16), q = l / 16), without LDS.  A work-group of NW waves takes 16 NB
 // columns (of one square) and splits K over its waves in runs of K-steps; the
 // loads of U steps are in flight per wave.  The waves' sums are added in wave
-// order through LDS, where the epilogue reads them row-wise.
+// order through LDS, where the epilogue reads them row-wise.  64 x 2048 x 7168
+// exact: 9.9 us again and again on the same operands, 14.5 in turn with others;
+// the weights' 15 MB are 3 of them, the rest a few loads' latency, one after the
+// other, and the sums.  64 rows over 128 experts of 1536 x 2048, 118 MB of weights
+// that have rows: 26 us (4.6 TB/s).
 template <int RT, int NB, int NW, int U, bool EXACT, int FA, int FB>
 __global__ void __launch_bounds__(NW * 64) block_skinny_kernel(BlockLinArgs p)
 {

@@ -14,8 +14,8 @@ namespace mxg {
 // next choice is the largest of the keys rounded to FP32, as the unsigned whole
 // numbers of the same order, over the lanes; only where several experts have it
 // are the keys themselves compared.  0 stands for an expert that is not chosen
-// (any more).  Bound by instructions: 16384 tokens of 256 experts in 8 groups,
-// sigmoid, k 8, read 17 MB.
+// (any more).  Few tokens are bound by one wave's chain of steps, k times a
+// maximum over the lanes: 4 tokens of 128 experts, k 8, take 3.8 us.
 
 __device__ __forceinline__ uint32_t ordered(float x)
 {
@@ -360,6 +360,9 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs p)
 // are whole lanes: a power of two of them each.  Keys are formed in FP32 first.
 // Only where a choice hangs on less than they are good for, two keys or two
 // groups' ranks nearer than `Near` says, does the wave choose by keys in 64 bits.
+// (16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 25 us, bound by
+// its instructions, since 18 MB move.  With the gradient's kernel of this kind 35
+// us, against 48 with a wave to a token in both.)
 struct Near {
     float part, floor;
     __device__ __forceinline__ explicit Near(const RouteArgs& p)
@@ -628,8 +631,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
 // Gradient to the logits, with g_j = scale d_weights_j and w the weights over
 // their scale: normalised softmax w_j (g_j - <g w>); softmax s_e (g_e - <g s>)
 // over all experts; sigmoid g_j s_j (1 - s_j), normalised with (g_j - <g w>) /
-// sum s for g_j.  A wave takes a token; choice j in lane j.  ALL: every logit
-// has a gradient (softmax that is not normalised).
+// sum s for g_j.  In 64 bits: g - <g w> cancels where one choice has all weight.
+
 // The gradient of one choice: lane j of those that share a token has its logit,
 // g_j and whether it was chosen; sums over them by `sum`, maximum by `largest`.
 template <class Sum, class Max>
@@ -653,7 +656,7 @@ __device__ __forceinline__ double choice_gradient(const RouteArgs& p, float logi
 // Where only the chosen logits have a gradient, sixteen lanes per token as above:
 // choice j in lane j, whose gradient goes to the token's row in LDS one choice
 // after the other (an index given twice counts twice), and the row from there to
-// memory.
+// memory.  16384 tokens of 256 experts, k 8: 10.4 us, where 26 MB move (2.5 TB/s).
 template <int S>
 __global__ void __launch_bounds__(256) route_rows_backward_kernel(RouteArgs p)
 {
@@ -716,6 +719,8 @@ __global__ void __launch_bounds__(256) route_rows_backward_kernel(RouteArgs p)
     }
 }
 
+// A wave takes a token; choice j in lane j.  ALL: every logit has a gradient
+// (softmax that is not normalised).
 template <int S, bool ALL>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs p)
 {
