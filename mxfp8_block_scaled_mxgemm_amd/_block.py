@@ -80,6 +80,15 @@ def _new(shape, dtype, device):
     return _moe.torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
 
 
+def _new_scales(rows, blocks, device):
+    """Scales [rows, blocks], block by block in memory."""
+    return _moe.torch.empty_strided((rows, blocks), (1, rows or 1), dtype=_moe.torch.float32, device=device)
+
+
+def _vector(n, dtype, device):
+    return _moe.torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
 def _matrix(t, name, device=None, dtypes=None, shape=None):
     ld = _rows_of(t, name, device, dtypes, shape)
     if t.dim() != 2:
@@ -163,14 +172,14 @@ def _quantize(x, z, act, gated, sort, fmt, rows, cols):
     fmt, act = _format(fmt), _activation(act)
     q = s = qt = st = None
     if rows:
-        q, s = _new((M, Cp), torch.uint8, dev), _new((Cp // STEP, M), torch.float32, dev)
+        q, s = _new((M, Cp), torch.uint8, dev), _new_scales(M, Cp // STEP, dev)
     if cols:
-        qt, st = _new((C, ld_qt), torch.uint8, dev), _new((ld_qt // STEP, C), torch.float32, dev)
+        qt, st = _new((C, ld_qt), torch.uint8, dev), _new_scales(C, ld_qt // STEP, dev)
     _run(_load().mxgemm_block_quantize, dev, x.data_ptr(), _TYPES[x.dtype], ld_x,
          None if z is None else z.data_ptr(), ld_z, M, C, act, 1 if gated else 0, off or None, koff or None, E, fmt,
          None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
          None if qt is None else qt.data_ptr(), None if st is None else st.data_ptr(), ld_qt)
-    return (q, None if s is None else s.t()), (qt, None if st is None else st.t())
+    return (q, s), (qt, st)
 
 
 @_on_stream
@@ -278,7 +287,7 @@ def _linear(a, a_scale, w, w_scale, offsets, mode, out_dtype, precision, a_fmt, 
     if mode == GROUP_NONE and not (squares and M <= 64 and -(-M // 32) * -(-N // 16) <= 256 and tile_cfg < 0):
         work = _split_workspace(M, N, K)
     if work:
-        work_mem = torch.empty(work, dtype=torch.uint8, device=dev)
+        work_mem = _vector(work, torch.uint8, dev)
         work_ptr = work_mem.data_ptr()
     # (the only expert's stride may be anything)
     w_group, ws_group = (w.stride(0), w_scale.stride(0)) if by_row and E > 1 else (0, 0)
@@ -428,15 +437,17 @@ def add_norm_backward(d_y, d_r, x, r, gate=None, scale: float = 1.0, post_weight
     pre, pre_type = _weight(pre_weight, "pre_weight", dev, H)
     d_x = _new((T, H), x.dtype, dev)
     d_res = _new((T, H), x.dtype, dev) if residual else None
-    d_gate = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-    sums = _new((2, H), torch.float32, dev)
+    d_gate = None
+    if gate is not None:
+        d_gate = _vector(H, gate.dtype, dev) if gate.dim() == 1 else _new((G, H), gate.dtype, dev)
+    d_post = _vector(H, torch.float32, dev) if post else None
+    d_pre = _vector(H, torch.float32, dev) if pre else None
     lib = _load()
     size = lib.mxgemm_add_norm_workspace(T, H, G)
-    work = torch.empty(size, dtype=torch.uint8, device=dev)
+    work = _vector(size, torch.uint8, dev)
     ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
     _run(lib.mxgemm_add_norm_backward, dev, NORM_ARGS.pack(
         x.data_ptr(), 0, g_ptr, post, pre, r.data_ptr(), 0, ptr(d_y), ptr(d_r), d_x.data_ptr(), ptr(d_res),
-        ptr(d_gate), sums.data_ptr(), sums.data_ptr() + 4 * H, work.data_ptr(), size, T, H, G, ld_x, 0, ld_g, ld_r, 0,
+        ptr(d_gate), ptr(d_post), ptr(d_pre), work.data_ptr(), size, T, H, G, ld_x, 0, ld_g, ld_r, 0,
         ld_dy, ld_dr, H, H, _TYPES[x.dtype], g_type, post_type, pre_type, _pick(NORMS, kind, "norm"), scale, eps, 0))
-    return NormGrads(d_x, d_res, d_gate, None if post_weight is None else sums[0],
-                     None if pre_weight is None else sums[1])
+    return NormGrads(d_x, d_res, d_gate, d_post, d_pre)
