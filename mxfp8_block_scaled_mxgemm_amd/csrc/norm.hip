@@ -278,8 +278,9 @@ __device__ __forceinline__ void store_part(const NormArgs& p, int which, int64_t
 // its columns' sums in registers and leaves them as one partial row, which
 // norm_sums_kernel adds in order.  8192 x 4096 bfloat16 with everything and 8 gate
 // rows: 430 MB, 25 of them partial rows, in 108 us (4.0 TB/s), and 7 for the sums.
-// A row's four trips over lanes and LDS are what the waves wait for; 128 registers
-// hold no row ahead at this width.
+// 128 registers hold no row ahead at this width, so that a row's loads and its
+// arithmetic follow each other within a wave; its four trips over lanes and LDS
+// merged into two took as long.
 template <int TYPE, bool WHOLE>
 struct NormInputs {
     RawRow<TYPE, WHOLE> dy, dr, x, r;
