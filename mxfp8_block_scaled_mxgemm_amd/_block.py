@@ -175,8 +175,11 @@ def _quantize(x, z, act, gated, sort, fmt, rows, cols):
         q, s = _new((M, Cp), torch.uint8, dev), _new_scales(M, Cp // STEP, dev)
     if cols:
         qt, st = _new((C, ld_qt), torch.uint8, dev), _new_scales(C, ld_qt // STEP, dev)
+    if M == 0 and not (cols and sort is not None):      # nothing to write
+        return (q, s), (qt, st)
+    # (an empty z has no address, and none stands for the forward form: any other does)
     _run(_load().mxgemm_block_quantize, dev, x.data_ptr(), _TYPES[x.dtype], ld_x,
-         None if z is None else z.data_ptr(), ld_z, M, C, act, 1 if gated else 0, off or None, koff or None, E, fmt,
+         None if z is None else z.data_ptr() or koff, ld_z, M, C, act, 1 if gated else 0, off or None, koff or None, E, fmt,
          None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
          None if qt is None else qt.data_ptr(), None if st is None else st.data_ptr(), ld_qt)
     return (q, s), (qt, st)

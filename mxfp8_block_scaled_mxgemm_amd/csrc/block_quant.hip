@@ -377,7 +377,7 @@ __device__ __forceinline__ void clear_rest(const BlockQuantArgs& p, int chunk, i
         if (tid < cols)
             p.st[(int64_t)chunk * p.C + tc * kTile + tid] = 0.f;
     }
-    if (!p.q)
+    if (!p.q || p.rows == 0)
         return;
     // the chunks past the last segment share the dropped rows
     int first = p.k_offsets[p.groups], live = p.offsets[p.groups];
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) b
         if (p.offsets)
             live = min(max(p.offsets[p.groups], 0), p.rows);
     } else {
-        if (!segment_rows(p, chunk, row0, end)) {
+        if (p.rows == 0 || !segment_rows(p, chunk, row0, end)) {   // (no row may be read)
             clear_rest(p, chunk, tc);
             return;
         }
@@ -470,7 +470,7 @@ block_quant_pair_kernel(BlockQuantArgs p)
         if (p.offsets)
             live = min(max(p.offsets[p.groups], 0), p.rows);
     } else {
-        if (!segment_rows(p, chunk, row0, end)) {
+        if (p.rows == 0 || !segment_rows(p, chunk, row0, end)) {   // (no row may be read)
             if (tid < 256) {
                 clear_rest(p, chunk, tc);
                 clear_rest(p, chunk, tc + tiles);

@@ -207,6 +207,14 @@ def test_quantize_strides_streams_and_none():
     sort = pkg.sort_tokens(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 3)
     (q, s), (qt, st) = pkg.block_quantize(x[:0], cols=True, sort=sort)
     assert qt.shape == (200, 384) and not qt.any() and not st.any()
+    # segments where there are no rows
+    bad = sort._replace(k_offsets=torch.tensor([0, 128, 128, 384], dtype=torch.int32, device="cuda"))
+    for act, gated in (("none", False), ("silu", True)):
+        _, (qt, st) = pkg.block_quantize(x[:0], act=act, gated=gated, cols=True, sort=bad)
+        assert not qt.any() and not st.any()
+    _, (qt, st) = pkg.block_quantize_backward(x[:0, :128], torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"),
+                                              act="silu", gated=True, sort=bad)
+    assert not qt.any() and not st.any()
 
 
 # ---------------------------------------------------------------- products --
