@@ -275,3 +275,41 @@ def test_steps_on_two_streams_at_once():
                 graph.replay()
         torch.cuda.synchronize()
         assert all(_same(out, refs[i]) for i, (_, out) in enumerate(graphs))
+
+
+def test_a_layer_without_tokens():
+    torch_cuda()
+    g = torch.Generator().manual_seed(3)
+    layer = Layer(g, 0, 256, 128, 4, 2, 2)
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    say("layer of no tokens")
+    f = layer.forward(x, x)
+    d = layer.backward(f, x)
+    assert f["r2"].shape == (0, 256) and f["ids"].shape == (0, 2)
+    for name, shape in (("w1", (4, 256, 256)), ("w2", (4, 256, 128)), ("wr", (4, 256))):
+        assert d[name].shape == shape and not d[name].any(), name
+    for grad in (d["n1"].d_gate, d["n1"].d_post_weight, d["n1"].d_pre_weight, d["n2"].d_gate, d["n2"].d_post_weight):
+        assert not grad.any()
+
+
+def test_every_token_dropped():
+    """No logit can be chosen: ids of -1, empty segments, zeros on the way back."""
+    torch_cuda()
+    g = torch.Generator().manual_seed(5)
+    T, H, F, E = 40, 256, 128, 4
+    layer = Layer(g, T, H, F, E, 2, 1)
+    x = torch.randn(T, H, generator=g).bfloat16().cuda()
+    say("layer of dropped tokens")
+    ids, weights = pkg.route_tokens(torch.full((T, E), float("-inf"), device="cuda"), 2, **layer.route)
+    assert (ids == -1).all() and not weights.any()
+    s = pkg.sort_tokens(ids, E)
+    rows = pkg.dispatch_tokens(x, s)
+    a, at = pkg.block_quantize(rows, sort=s, cols=True)
+    z = pkg.block_linear(*a, *layer.w1, s.offsets)
+    b, bt = pkg.block_quantize(z, act="silu", gated=True, sort=s, cols=True)
+    out = pkg.combine_tokens(pkg.block_linear(*b, *layer.w2, s.offsets), s, weights)
+    assert not z.any() and not out.any()
+    d_b, d_w2 = pkg.block_linear_backward(rows, None, *bt, *layer.w2t, sort=s)
+    d_rows, d_w1 = pkg.block_linear_backward(d_b, z, *at, *layer.w1t, act="silu", gated=True, sort=s)
+    assert not d_b.any() and not d_rows.any() and not d_w1.any() and not d_w2.any()
+    assert not pkg.route_tokens_backward(weights, torch.zeros(T, E, device="cuda"), ids, score="sigmoid").any()
