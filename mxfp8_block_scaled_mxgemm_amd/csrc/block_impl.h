@@ -465,10 +465,11 @@ __device__ __forceinline__ void block_epilogue(const BlockLinArgs& p, uint8_t* m
 //
 // Tiles of 128 x 128 keep the simple loop: two work-groups on a compute unit fill
 // each other's waits (8192 x 8192 x 8192 native 562 us, 572 with the loop above;
-// exact 935, 1.18 PFLOP/s, where a plain BF16 product reaches 1.25).  Neither more
-// stages with one work-group (256 x 128 in three, 592; 128 x 128 in four, 959) nor
-// fragments read a step ahead there (909) do as well, and for 512 x 4096 x 4096,
-// whose 128 work-groups are alone, those took 32 us and this loop 26.
+// exact 935, 1.18 PFLOP/s, where a plain BF16 product reaches 1.25).  More stages
+// with one work-group (256 x 128 in three, 592; 128 x 128 in four, 959, with eight
+// waves 743, with fragments read a step ahead 909) or eight waves in each of two
+// (567) did no better.  Where work-groups are alone (256 x 4096 x 4096 native, 64
+// of them: 26 us) the copies by themselves take 22 and the arithmetic 20.
 template <int BM, int BN, int WGM, int WGN, int WGK, int WGS, bool EXACT, bool SQUARES, int FA, int FB>
 __global__ void __launch_bounds__(WGM * WGN * WGK * 64)
     __attribute__((amdgpu_waves_per_eu(WGM * WGN * WGK * WGS / 4, WGM * WGN * WGK * WGS / 4)))

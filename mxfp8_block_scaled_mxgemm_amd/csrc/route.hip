@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs p)
 // are whole lanes: a power of two of them each.  Keys are formed in FP32 first.
 // Only where a choice hangs on less than they are good for, two keys or two
 // groups' ranks nearer than `Near` says, does the wave choose by keys in 64 bits.
-// (16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 25 us, bound by
-// its instructions, since 18 MB move.  With the gradient's kernel of this kind 35
+// (16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 24 us, bound by
+// its instructions, since 18 MB move.  With the gradient's kernel of this kind 31
 // us, against 48 with a wave to a token in both.)
 struct Near {
     float part, floor;
@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
 {
     constexpr int kWide = S / 4;        // slots of a lane where the wave has one token
     __shared__ double lds[GROUPS ? 4 * 64 * kWide : 1];
+    __shared__ int32_t chosen[16][16];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, row = lane >> 4, l = lane & 15;
     const bool by_logit = !p.bias && !GROUPS;
     const int per = (p.experts + 15) / 16, first = per * l;
@@ -549,7 +550,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
                     near[s] = open && key[s] > -INFINITY ? ordered(key[s]) : 0;
             }
         }
-        int mine = -1;                  // choice j in lane j of the token's
+        int32_t* const list = chosen[4 * wave + row];       // choice j in place j
+        list[l] = -1;
+        __builtin_amdgcn_wave_barrier();
         uint32_t before = 0;
 #pragma unroll 1
         for (int j = 0; j <= p.k; ++j) {
@@ -567,13 +570,20 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
 #pragma unroll
             for (int s = S - 1; s >= 0; --s)
                 slot = near[s] == best ? s : slot;
-            // the lowest index that has it
-            const uint32_t e = ~row16_max(slot < 64 && best != 0 ? ~(uint32_t)(first + slot) : 0u);
-            mine = l == j && best != 0 ? (int)e : mine;
+            // the lowest index that has it: the first lane's
+            const bool has = slot < 64 && best != 0;
+            const uint32_t who = (uint32_t)(__ballot(has) >> (lane & 48));
+            const bool wins = has && (who & ((1u << l) - 1)) == 0;
+            if (wins)
+                list[j] = first + slot;
+            slot = wins ? slot : 64;
 #pragma unroll
             for (int s = 0; s < S; ++s)
-                near[s] = e == (uint32_t)(first + s) ? 0 : near[s];
+                near[s] = slot == s ? 0 : near[s];
         }
+        __builtin_amdgcn_wave_barrier();
+        int mine = list[l];
+        __builtin_amdgcn_wave_barrier();
         // the tokens in doubt, one at a time by the whole wave
         uint64_t rows = by_logit ? 0 : __ballot(doubt);
         while (rows) {
@@ -656,16 +666,14 @@ __device__ __forceinline__ double choice_gradient(const RouteArgs& p, float logi
 // Where only the chosen logits have a gradient, sixteen lanes per token as above:
 // choice j in lane j, whose gradient goes to the token's row in LDS one choice
 // after the other (an index given twice counts twice), and the row from there to
-// memory.  16384 tokens of 256 experts, k 8: 10.4 us, where 26 MB move (2.5 TB/s).
+// memory.  16384 tokens of 256 experts, k 8: 6.6 us, where 26 MB move (3.9 TB/s);
+// 10.4 with runs of sixteen experts a lane, which met in a few of LDS's banks.
 template <int S>
 __global__ void __launch_bounds__(256) route_rows_backward_kernel(RouteArgs p)
 {
     __shared__ __attribute__((aligned(16))) float lds[16][16 * S];
     const int l = threadIdx.x & 15, wave = threadIdx.x >> 6, row = (threadIdx.x & 63) >> 4;
     float* const mine = lds[4 * wave + row];
-    const int per = (p.experts + 15) / 16, first = per * l;
-    const int count = p.experts - first < per ? p.experts - first : per;
-    const bool whole = per == S && p.experts == 16 * S;
     for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4; t0 < p.tokens; t0 += (int64_t)gridDim.x * 16) {
         const bool real = t0 + row < p.tokens;
         const int64_t t = real ? t0 + row : p.tokens - 1;
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(256) route_rows_backward_kernel(RouteArgs p)
                                                [](float v) { return row16_max_logit(v); });
 #pragma unroll
         for (int s = 0; s < S; s += 4)
-            *reinterpret_cast<v4f*>(mine + S * l + s) = v4f{0.f, 0.f, 0.f, 0.f};
+            *reinterpret_cast<v4f*>(mine + 16 * s + 4 * l) = v4f{0.f, 0.f, 0.f, 0.f};
         // (the lanes of a wave meet only their own wave's rows, whose LDS
         // operations complete in order)
         __builtin_amdgcn_wave_barrier();
@@ -687,27 +695,32 @@ __global__ void __launch_bounds__(256) route_rows_backward_kernel(RouteArgs p)
                 mine[id] += d;
             __builtin_amdgcn_wave_barrier();
         }
-        float out[S];
+        // (four experts a lane, so that a token's lanes read and write a run)
+        v4f out[S / 4];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-            out[s] = mine[s < count ? first + s : 0];
+        for (int s = 0; s < S / 4; ++s)
+            out[s] = *reinterpret_cast<const v4f*>(mine + 64 * s + 4 * l);
         __builtin_amdgcn_wave_barrier();
         if (!real)
             continue;
         auto put = [&](auto tc) __attribute__((always_inline)) {
             constexpr int TYPE = decltype(tc)::value;
-            typename Element<TYPE>::T* to = static_cast<typename Element<TYPE>::T*>(p.d_logits) + t * p.ld_d + first;
-            if (whole) {
-                Pack<TYPE, S> v;
+            typename Element<TYPE>::T* to = static_cast<typename Element<TYPE>::T*>(p.d_logits) + t * p.ld_d;
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    v.put(s, out[s]);
-                v.store(to);
-            } else {
+            for (int s = 0; s < S / 4; ++s) {
+                const int c = 64 * s + 4 * l;
+                if (c + 4 <= p.experts) {
+                    Pack<TYPE, 4> v;
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (s < count)
-                        to[s] = Element<TYPE>::put(out[s]);
+                    for (int u = 0; u < 4; ++u)
+                        v.put(u, out[s][u]);
+                    v.store(to + c);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (c + u < p.experts)
+                            to[c + u] = Element<TYPE>::put(out[s][u]);
+                }
             }
         };
         if (p.type == kFP32)
