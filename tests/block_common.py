@@ -73,9 +73,9 @@ def value(q, s, fmt):
 def check_blocks(q, s, y, t, fmt, what):
     """Codes q [R, Cp] and scales s [R, Cp / 128] hold y [R, C] (64-bit, known to
     t): each scale the largest magnitude over the format's (one division), each
-    value within half a code's step.  The code is rounded from y times a factor
-    rounded once, so both roundings (and the scale's) may move it across a tie:
-    3 U of the value."""
+    value within half a code's step.  The quotient's own roundings, and the one
+    of the scale that the value is formed with here, may move it across a tie: 3
+    U of the value."""
     q, s = q.cpu(), s.cpu()
     R, C = y.shape
     Cp = up(C)
