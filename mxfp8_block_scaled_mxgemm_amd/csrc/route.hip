@@ -374,31 +374,24 @@ struct Near {
         part = p.sigmoid ? 1.f / (1 << 20) : 1.f / (1 << 16);
         floor = p.bias ? 1.f : 1e-26f;
     }
+    // (also where both are infinite, whose difference is none)
     __device__ __forceinline__ bool doubt(float a, float b) const
     {
-        return fabsf(a - b) <= part * (fabsf(a) + floor);
+        return !(fabsf(a - b) > part * (fabsf(a) + floor));
     }
 };
 
-template <int CTRL, class T>
-__device__ __forceinline__ T dpp_any(T x)
+template <int CTRL>
+__device__ __forceinline__ void top_two(float& a, float& b)
 {
-    if constexpr (sizeof(T) == 8)
-        return dpp64<CTRL>(x);
-    else
-        return dpp<CTRL>(x);
+    const float a1 = dpp<CTRL>(a), b1 = dpp<CTRL>(b);
+    b = fmaxf(fmaxf(b, b1), fminf(a, a1));
+    a = fmaxf(a, a1);
 }
-template <int CTRL, class T>
-__device__ __forceinline__ void top_two(T& a, T& b)
-{
-    const T a1 = dpp_any<CTRL>(a), b1 = dpp_any<CTRL>(b);
-    b = max(max(b, b1), min(a, a1));
-    a = max(a, a1);
-}
-// A group's rank from its lanes' two largest keys.  (A group of whom one can be
-// chosen has that one's key.)
-template <class T>
-__device__ __forceinline__ T group_rank(int lanes, T a, T b)
+// Half of a group's rank, from its lanes' two largest keys: the sum of two large
+// biases would leave FP32's range.  (A group of whom one can be chosen has that
+// one's key.)
+__device__ __forceinline__ float half_rank(int lanes, float a, float b)
 {
     if (lanes >= 2)
         top_two<kDppSwap1>(a, b);
@@ -406,7 +399,7 @@ __device__ __forceinline__ T group_rank(int lanes, T a, T b)
         top_two<kDppSwap2>(a, b);
     if (lanes >= 8)
         top_two<kDppHalfMirror>(a, b);
-    return b > -INFINITY ? a + b : a;
+    return b > -INFINITY ? 0.5f * a + 0.5f * b : 0.5f * a;
 }
 
 __device__ __forceinline__ double row16_sum(double x)
@@ -535,13 +528,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
                 }
                 bool open = true;
                 if constexpr (GROUPS) {
-                    const float rank = group_rank(lanes, a, b);
+                    const float rank = half_rank(lanes, a, b);
                     int ahead = 0;
 #pragma unroll 1
                     for (int h = 0; h < p.groups; ++h) {
                         const float other = __shfl(rank, (threadIdx.x & 48) + h * lanes);
                         ahead += other > rank ? 1 : 0;
-                        doubt |= h != l / lanes && rank > -INFINITY && close.doubt(0.5f * rank, 0.5f * other);
+                        doubt |= h != l / lanes && rank > -INFINITY && close.doubt(rank, other);
                     }
                     open = ahead < p.top_groups;
                 }
