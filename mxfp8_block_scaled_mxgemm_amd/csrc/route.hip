@@ -370,14 +370,18 @@ struct Near {
         // sigmoids are good to four steps; a softmax's exponents, differences of
         // logits down to -70, carry their own rounding: 70 2^-24 each.  A bias
         // may cancel a score, at most 1; without one, scores below 1e-30 are
-        // all in doubt, since FP32 soon ends there.
+        // all in doubt, since FP32 soon ends there.  In all, a sigmoid's key is off
+        // by 6 2^-24 of the score and 2^-24 of itself at most, half a rank by half
+        // of its two keys' errors and 2^-24 of itself; two of them by less than 16
+        // 2^-24 = 2^-20 of 1 (or the score) and of the magnitudes in them.
         part = p.sigmoid ? 1.f / (1 << 20) : 1.f / (1 << 16);
         floor = p.bias ? 1.f : 1e-26f;
     }
-    // (also where both are infinite, whose difference is none)
-    __device__ __forceinline__ bool doubt(float a, float b) const
+    // a and b are sums of magnitudes up to `size` (also where both are infinite,
+    // whose difference is none)
+    __device__ __forceinline__ bool doubt(float a, float b, float size) const
     {
-        return !(fabsf(a - b) > part * (fabsf(a) + floor));
+        return !(fabsf(a - b) > part * (size + floor));
     }
 };
 
@@ -390,8 +394,9 @@ __device__ __forceinline__ void top_two(float& a, float& b)
 }
 // Half of a group's rank, from its lanes' two largest keys: the sum of two large
 // biases would leave FP32's range.  (A group of whom one can be chosen has that
-// one's key.)
-__device__ __forceinline__ float half_rank(int lanes, float a, float b)
+// one's key.)  size: the magnitudes in it, to which its error is relative: a large
+// bias and its negative leave a small rank with a large error.
+__device__ __forceinline__ float half_rank(int lanes, float a, float b, float& size)
 {
     if (lanes >= 2)
         top_two<kDppSwap1>(a, b);
@@ -399,7 +404,9 @@ __device__ __forceinline__ float half_rank(int lanes, float a, float b)
         top_two<kDppSwap2>(a, b);
     if (lanes >= 8)
         top_two<kDppHalfMirror>(a, b);
-    return b > -INFINITY ? 0.5f * a + 0.5f * b : 0.5f * a;
+    const bool two = b > -INFINITY;
+    size = 0.5f * fabsf(a) + (two ? 0.5f * fabsf(b) : 0.f);
+    return two ? 0.5f * a + 0.5f * b : 0.5f * a;
 }
 
 __device__ __forceinline__ double row16_sum(double x)
@@ -528,13 +535,14 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
                 }
                 bool open = true;
                 if constexpr (GROUPS) {
-                    const float rank = half_rank(lanes, a, b);
+                    float size;
+                    const float rank = half_rank(lanes, a, b, size);
                     int ahead = 0;
 #pragma unroll 1
                     for (int h = 0; h < p.groups; ++h) {
                         const float other = __shfl(rank, (threadIdx.x & 48) + h * lanes);
                         ahead += other > rank ? 1 : 0;
-                        doubt |= h != l / lanes && rank > -INFINITY && close.doubt(rank, other);
+                        doubt |= h != l / lanes && rank > -INFINITY && close.doubt(rank, other, size);
                     }
                     open = ahead < p.top_groups;
                 }
@@ -555,7 +563,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
                 best = max(best, near[s]);
             best = row16_max(best);
             if (!by_logit && j > 0 && best != 0)
-                doubt |= close.doubt(from_ordered(before), from_ordered(best));
+                doubt |= close.doubt(from_ordered(before), from_ordered(best), fabsf(from_ordered(before)));
             before = best;
             if (j == p.k)               // only whether the last choice is certain
                 break;

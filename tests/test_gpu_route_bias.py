@@ -52,3 +52,20 @@ def test_infinite_and_huge_biases(E, k, groups, top, score):
         say(f"{name} E={E} k={k} groups={groups}/{top} {score}")
         _same_choice(x, k, 24, score=score, bias=bias.cuda(), groups=groups, top_groups=top)
         _same_choice(x, k, 24, score=score, bias=bias.cuda())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [64.0, 256.0, 1e4, 1e6])
+@pytest.mark.parametrize("E,k,groups,top", [(16, 8, 8, 4), (128, 4, 8, 2)])
+def test_biases_that_cancel_in_a_rank(E, k, groups, top, size, score):
+    """A group's two largest keys hold a large bias and its negative: their sum is
+    as small as the scores, its rounding in FP32 as large as the bias."""
+    torch_cuda()
+    g = torch.Generator(device="cuda").manual_seed(E)
+    T = 1 << (20 if E == 16 else 17)
+    x = torch.randn(T, E, generator=g, device="cuda")
+    bias = torch.full((E,), -2 * size, device="cuda")
+    run = E // groups
+    bias[::run], bias[1::run] = size, -size
+    say(f"cancel E={E} +-{size:g} {score}")
+    _same_choice(x, k, 24, score=score, bias=bias, groups=groups, top_groups=top)
