@@ -169,12 +169,14 @@ __device__ __forceinline__ void put_columns(const uint8_t* codes, uint8_t* out, 
 
 // ----------------------------------------------------------- activations ----
 
-// silu and its derivative a rounding or two from exact: a code hangs on which
-// side of a tie y lies, so errors of the shared, faster form (an exponential
-// that carries its argument's rounding) show as codes that differ: twice as
-// many from the exact ones' as this form has.  exp(-z) as 2^h (1 + l ln 2), h
-// and l the product -z log2 e in two parts; the reciprocal with one Newton step.
-__device__ __forceinline__ float sigmoid_near(float z)
+// silu and its derivative a few roundings from exact: a code hangs on which side of
+// a tie y lies, so errors of the shared, faster form (an exponential that carries
+// its argument's rounding) show as codes that differ: twice as many from the exact
+// ones' as this form has.  exp(-z) as 2^h (1 + l ln 2), h and l the product -z log2
+// e in two parts; the reciprocal with one Newton step.  rest: 1 - the sigmoid, for
+// z > 2 from the exponential, since the difference loses the sigmoid's rounding
+// times z to the derivative (16 roundings of that at z = 16).
+__device__ __forceinline__ float sigmoid_near(float z, float& rest)
 {
     constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147181f;
     const float h = -z * kHi, l = fmaf(-z, kHi, -h) - z * kLo;
@@ -182,15 +184,20 @@ __device__ __forceinline__ float sigmoid_near(float z)
     const float far = __builtin_amdgcn_rcpf(1.f + e);       // 0 or 1, or NaN
     e = fmaf(e, l * kLn2, e);
     const float d = 1.f + e, r = __builtin_amdgcn_rcpf(d);
-    return fabsf(h) < 126.f ? fmaf(fmaf(-d, r, 1.f), r, r) : far;
+    const bool near = fabsf(h) < 126.f;
+    const float s = near ? fmaf(fmaf(-d, r, 1.f), r, r) : far;
+    rest = near && z > 2.f ? e * s : 1.f - s;
+    return s;
 }
 
 __device__ __forceinline__ void activate8(int act, float (&z)[8])
 {
     if (act == kActSilu) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            z[u] *= sigmoid_near(z[u]);
+        for (int u = 0; u < 8; ++u) {
+            float rest;
+            z[u] *= sigmoid_near(z[u], rest);
+        }
     } else {
         activate(act, z);
     }
@@ -202,9 +209,10 @@ __device__ __forceinline__ void activate_grads8(int act, float (&z)[8], float (&
     if (act == kActSilu) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float s = sigmoid_near(z[u]);
+            float rest;
+            const float s = sigmoid_near(z[u], rest);
             y[u] = z[u] * s;
-            z[u] = s * (1.f + z[u] * (1.f - s));
+            z[u] = s * fmaf(z[u], rest, 1.f);
         }
     } else {
         activate_grads(act, z, y);
