@@ -72,7 +72,7 @@ def _pick(table, name, what):
     try:
         return table[name]
     except (KeyError, TypeError):
-        raise ValueError(f"unknown {what} {name!r}: one of {', '.join(table)}") from None
+        raise ValueError(f"unknown {what} {name!r}: one of {', '.join(map(str, table))}") from None
 
 
 def _new(shape, dtype, device):
