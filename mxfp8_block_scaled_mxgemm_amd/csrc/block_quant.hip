@@ -241,10 +241,21 @@ struct Raw {
     }
 };
 
+template <int N>
+__device__ __forceinline__ void clear(float (&v)[N][8])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[i][u] = 0.f;
+}
+
 // The thread's eight rows of y from `row` on, columns c .. c + 7, where a row
 // comes in whole eights: the loads of kBatch rows go out before the first is
 // used.  Rows from `live` and columns from C on are zero; what is loaded there
-// is the last row, or the last eight columns, there is.
+// is the last row, or the last eight columns, there is (a row below `live` must be
+// one of the tile's).
 template <int TYPE, bool BACK>
 __device__ __forceinline__ void values8x8(const BlockQuantArgs& p, int64_t row, int64_t live, int c, float (&v)[8][8])
 {
@@ -261,7 +272,7 @@ __device__ __forceinline__ void values8x8(const BlockQuantArgs& p, int64_t row, 
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             int64_t r = row + i0 + i;
-            r = r < live ? r : live > 0 ? live - 1 : 0;
+            r = r < live ? r : live - 1;
             x[i].load(p.x, r * p.ld_x + cc);
             if constexpr (BACK) {
                 z[i].load(p.z, r * p.ld_z + cc);
@@ -421,7 +432,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) b
     const int64_t row = row0 + 8 * (tid >> 4);
     float v[8][8];
     if constexpr (VEC) {
-        values8x8<TYPE, BACK>(p, row, live, c, v);
+        if (row0 < live)
+            values8x8<TYPE, BACK>(p, row, live, c, v);
+        else            // of a tile of dropped rows nothing is read
+            clear(v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -491,30 +505,35 @@ block_quant_pair_kernel(BlockQuantArgs p)
     const int64_t row = row0 + 4 * (tid >> 4);
     float v[4][8], w[4][8];
     constexpr int kBatch = TYPE == kFP32 ? 1 : 2;       // rows whose loads go out together
+    if (row0 >= live) {         // of a tile of dropped rows nothing is read
+        clear(v);
+        clear(w);
+    } else {
 #pragma unroll
-    for (int i0 = 0; i0 < 4; i0 += kBatch) {
-        Raw<TYPE> x[kBatch];
-        Raw<kBF16> g[kBatch], u[kBatch];
+        for (int i0 = 0; i0 < 4; i0 += kBatch) {
+            Raw<TYPE> x[kBatch];
+            Raw<kBF16> g[kBatch], u[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            int64_t r = row + i0 + i;
-            r = r < live ? r : live > 0 ? live - 1 : 0;
-            x[i].load(p.x, r * p.ld_x + c);
-            g[i].load(p.z, r * p.ld_z + c);
-            u[i].load(p.z, r * p.ld_z + p.half + c);
-        }
+            for (int i = 0; i < kBatch; ++i) {
+                int64_t r = row + i0 + i;
+                r = r < live ? r : live - 1;
+                x[i].load(p.x, r * p.ld_x + c);
+                g[i].load(p.z, r * p.ld_z + c);
+                u[i].load(p.z, r * p.ld_z + p.half + c);
+            }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            float d[8], s[8], a[8], y[8];
-            x[i].get(d);
-            g[i].get(s);
-            u[i].get(y);
-            activate_grads8(p.act, s, a);
-            const bool ok = row + i0 + i < live;
+            for (int i = 0; i < kBatch; ++i) {
+                float d[8], s[8], a[8], y[8];
+                x[i].get(d);
+                g[i].get(s);
+                u[i].get(y);
+                activate_grads8(p.act, s, a);
+                const bool ok = row + i0 + i < live;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[i0 + i][k] = ok ? d[k] * s[k] * y[k] : 0.f;
-                w[i0 + i][k] = ok ? d[k] * a[k] : 0.f;
+                for (int k = 0; k < 8; ++k) {
+                    v[i0 + i][k] = ok ? d[k] * s[k] * y[k] : 0.f;
+                    w[i0 + i][k] = ok ? d[k] * a[k] : 0.f;
+                }
             }
         }
     }
