@@ -278,6 +278,10 @@ def _linear(a, a_scale, w, w_scale, offsets, mode, out_dtype, precision, a_fmt, 
     squares = mode != GROUP_INNER and w_scale.shape == square
     E = off = 0
     if mode != GROUP_NONE:
+        if not isinstance(offsets, torch.Tensor):
+            raise TypeError(f"offsets: expected a tensor on {dev}")
+        if offsets.dim() != 1:
+            raise ValueError(f"offsets: expected [experts + 1], got {tuple(offsets.shape)}")
         E = lead[0] if by_row else offsets.shape[0] - 1
         off = _plain(offsets, "offsets", dev, torch.int32, (E + 1,))
         if E < 1:
