@@ -64,7 +64,7 @@ int mxgemm_route_tokens_backward(const float* d_weights, const void* logits, int
  *   s = max(amax / fmax, 2^-126),  q = y / s rounded to nearest even
  * (fmax 448 or 57344; q from the quotient with s before its rounding, itself
  * rounded to float32).  A block that holds a NaN or an infinity has scale NaN
- * and codes 0x7F.  Quantised is, in FP32,
+ * and codes 0x7F, those past the matrix's edge too.  Quantised is, in FP32,
  *   z NULL: y = act(x), or, gated, act(x[:, :C]) * x[:, C:] with x [rows][2 C]
  *   else:   y = x act'(z), or, gated, [x u act'(g), x act(g)] with [g, u] = z
  *           (z bfloat16 [rows][C]; x [rows][C], gated [rows][C / 2])
@@ -90,9 +90,10 @@ int mxgemm_block_quantize(const void* x, int32_t type, int64_t ld_x, const void*
 
 /* Weights w [batch][N][K] (row stride ld, matrix stride group, elements) with
  * one scale for each square of 128 x 128: codes q [batch][N][Kp], scales s
- * [batch][Np / 128][Kp / 128], Np and Kp rounded up to 128 (zeros past K); and
- * of the transposed weights (the same squares) qt [batch][K][Np], st
- * [batch][Kp / 128][Np / 128], or NULL.
+ * [batch][Np / 128][Kp / 128], Np and Kp rounded up to 128 (zeros past K; a square
+ * that holds a NaN or an infinity as a block that does); and of the transposed
+ * weights (the same squares) qt [batch][K][Np], st [batch][Kp / 128][Np / 128], or
+ * NULL.
  * Errors: EINVAL, EUNSUPPORTED (more than 65535 matrices or rows of squares). */
 int mxgemm_block_quantize_weight(const void* w, int32_t type, int64_t ld, int64_t group, int64_t batch, int64_t N,
                                  int64_t K, int32_t format, uint8_t* q, float* s, uint8_t* qt, float* st, void* stream);

@@ -194,7 +194,7 @@ def block_quantize(x, act="none", gated=False, sort: Optional[TokenSort] = None,
     q [M, Cp] (uint8 codes, zeros past C) and s [M, Cp / 128] are blocked along
     the columns; qt [C, Mp] and st [C, Mp / 128] hold y^T, blocked along the
     rows.  Cp, Mp: rounded up to 128.  A scale is the block's largest magnitude
-    over the format's; blocks with a NaN or an infinity are all NaN.  The
+    over the format's; blocks with a NaN or an infinity are all NaN, past C too.  The
     scales are stored block by block (``s.t()`` is contiguous), as block_linear
     reads them fastest.  With ``sort`` (x in its row order) dropped rows count
     as zero, codes and scales, and every expert's rows are padded to 128 by

@@ -225,8 +225,9 @@ int plan_linear(mxg::BlockLinArgs* a, int cfg, int cus, int64_t workspace_bytes)
     a->tiles_n = (int)tiles_n;
     a->total_work = (int)work;
     // group width: about a square patch of tiles per XCD per round of
-    // resident work-groups; skinny tiles share no rows of w, so theirs run
-    // along N
+    // resident work-groups; skinny tiles of one row tile share no rows of w, so
+    // theirs run along N (with two, a column's land on different XCDs, each of
+    // which then reads its rows of w)
     const int64_t per_xcd = ((work < cus ? work : cus) + mxg::kNumXcd - 1) / mxg::kNumXcd / a->split;
     int64_t g = (int64_t)floor(sqrt((double)(per_xcd > 1 ? per_xcd : 1)));
     if (cfg >= mxg::kBlockRows32)
@@ -239,7 +240,8 @@ int plan_linear(mxg::BlockLinArgs* a, int cfg, int cus, int64_t workspace_bytes)
 
 // Rows of the gradient in units, each within one gate row's, and workers: at
 // most as many as 16 waves on each of 256 compute units (their registers allow
-// no more).  The workers' partial rows are the workspace.
+// no more; where a wave takes a row, up to 512 columns, they allow 12, and the
+// last workers start as others end).  The workers' partial rows are the workspace.
 void plan_norm(mxg::NormArgs* a, int64_t gate_rows)
 {
     const int64_t most = 256 * 16 * 64 / mxg::norm_threads(a->cols);

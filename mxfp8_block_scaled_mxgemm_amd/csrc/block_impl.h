@@ -583,9 +583,10 @@ block_linear_kernel(BlockLinArgs p)
 // loads of U steps are in flight per wave.  The waves' sums are added in wave
 // order through LDS, where the epilogue reads them row-wise.  64 x 2048 x 7168
 // exact: 9.9 us again and again on the same operands, 14.5 in turn with others;
-// the weights' 15 MB are 3 of them, the rest a few loads' latency, one after the
-// other, and the sums.  64 rows over 128 experts of 1536 x 2048, 118 MB of weights
-// that have rows: 26 us (4.6 TB/s).
+// the weights' 15 MB, which both row tiles read, each on an XCD of its own (30.1
+// MB), are 6 of these, the rest a few loads' latency, one after the other, and the
+// sums.  64 rows over 128 experts of 1536 x 2048, 118 MB of weights that have rows:
+// 26 us (4.6 TB/s).
 template <int RT, int NB, int NW, int U, bool EXACT, int FA, int FB>
 __global__ void __launch_bounds__(NW * 64) block_skinny_kernel(BlockLinArgs p)
 {

@@ -175,7 +175,8 @@ __device__ __forceinline__ void put_columns(const uint8_t* codes, uint8_t* out, 
 // ones' as this form has.  exp(-z) as 2^h (1 + l ln 2), h and l the product -z log2
 // e in two parts; the reciprocal with one Newton step.  rest: 1 - the sigmoid, for
 // z > 2 from the exponential, since the difference loses the sigmoid's rounding
-// times z to the derivative (16 roundings of that at z = 16).
+// times z to the derivative (16 roundings of that at z = 16).  gelu and gelu_tanh
+// keep the shared forms: another form of gelu spilled registers.
 __device__ __forceinline__ float sigmoid_near(float z, float& rest)
 {
     constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147181f;

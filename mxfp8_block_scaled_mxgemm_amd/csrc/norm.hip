@@ -498,7 +498,10 @@ static void norm_launch(const NormArgs& a, bool backward, int cus, hipStream_t s
         return;
     }
     int64_t groups = (a.rows + W::kPerGroup - 1) / W::kPerGroup;
-    const int64_t most = (int64_t)cus * (2048 / W::kThreads);       // as many as are resident
+    // as many as a compute unit has waves for; their registers let five to seven
+    // eighths of them be resident (three work-groups of 512 threads, one of 1024),
+    // and the others follow
+    const int64_t most = (int64_t)cus * (2048 / W::kThreads);
     groups = groups < most ? groups : most;
     hipLaunchKernelGGL((norm_kernel<TYPE, NT, WHOLE>), dim3((unsigned)groups), dim3(W::kThreads), 0, stream, a);
 }

@@ -360,9 +360,11 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs p)
 // are whole lanes: a power of two of them each.  Keys are formed in FP32 first.
 // Only where a choice hangs on less than they are good for, two keys or two
 // groups' ranks nearer than `Near` says, does the wave choose by keys in 64 bits.
-// (16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 24 us, bound by
-// its instructions, since 18 MB move.  With the gradient's kernel of this kind 31
-// us, against 48 with a wave to a token in both.)
+// 16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 22 to 24 us, where
+// the 18 MB that move take 3.5.  They are one generation of four waves per SIMD,
+// which wait 61% of their time for their own chains (of 65536 tokens, 68 us, each
+// 16384 more take 15).  With the gradient's kernel of this kind 29 us, against 48
+// with a wave to a token in both.
 struct Near {
     float part, floor;
     __device__ __forceinline__ explicit Near(const RouteArgs& p)
@@ -872,9 +874,14 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream)
     const int per = (a.experts + 15) / 16, size = a.experts / a.groups, lanes = size / per;
     const bool whole = a.groups == 1 || (size % per == 0 && (lanes & (lanes - 1)) == 0);
     // Few tokens wait for one wave's steps, which are fewer where it has one
-    // token: sigmoid and bias, 256 experts, k 8, a wave to a token / four tokens
-    // to a wave: 1024 tokens 7.8 / 11.5 us, 4096 11.1 / 11.9, 16384 28.4 / 18.7,
-    // 65536 102 / 53.
+    // token.  A wave to a token / four tokens to a wave, k 8, us at 4096, 16384 and
+    // 65536 tokens: 256 experts by their logits 6.7 / 6.7, 16.7 / 10.8, 57 / 33;
+    // by sigmoid and bias 8.1 / 12.2, 21.0 / 19.7, 74 / 54; in 8 groups 10.7 /
+    // 14.8, 29.5 / 23.9, 105 / 68; 64 experts in 4 groups, k 4, softmax and bias
+    // 6.3 / 7.3, 15.5 / 9.3, 50 / 23.  Where many tokens are in doubt the second
+    // catches up later: 16-bit logits in groups without a bias, whose equal keys
+    // all are (256 experts in 8 groups 10.9 / 27.1, 29.4 / 36.2, 104 / 102), and 16
+    // choices by softmax and bias (10.9 / 22.4, 28.0 / 33.7, 100 / 86).
     return a.experts <= 256 && a.k <= 16 && whole && a.tokens > 4096 ? route_rows(a, false, stream)
                                                                      : route_any(a, false, stream);
 }
