@@ -41,7 +41,8 @@ extern "C" {
  * (without bias and groups the logits themselves are).  An expert whose logit
  * or key is -infinity or NaN is never chosen; where fewer than k experts are
  * left the last ids are -1, with weight 0: pairs that mxgemm_sort_tokens drops.
- * A logit of +infinity counts as the largest finite number.
+ * A logit of +infinity counts as the largest finite number; sigmoids of logits
+ * below -700 are 0.
  * 1 <= experts <= 1024, 1 <= k <= min(experts, 64), groups <= 64 divides
  * experts, 1 <= top_groups <= groups, k <= top_groups * experts / groups.
  * Errors: EINVAL, EUNSUPPORTED, EHIP.

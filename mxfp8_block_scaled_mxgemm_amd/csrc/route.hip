@@ -658,7 +658,7 @@ __device__ __forceinline__ double choice_gradient(const RouteArgs& p, float logi
         if (!p.normalize)
             return g * slope;
         const double all = sum(score), dot = sum(g * score), part = all > 0.0 ? reciprocal64(all) : 0.0;
-        return (g - dot * part) * part * slope;
+        return (g - dot * part) * (part * slope);       // (1 / the sum may be 1e304)
     }
     const float base = largest(logit);
     const double e = exp64(has ? (double)logit - (double)base : 0.0), score = has ? e : 0.0;
