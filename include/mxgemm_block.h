@@ -152,9 +152,9 @@ int mxgemm_block_linear(const mxgemm_block_linear_t* args, void* stream);
  *   y = norm(r) pre_weight          (pre_weight NULL: no y)
  *   norm(v) = (v - m) / sqrt(mean((v - m)^2) + eps), m = 0 (RMS) or v's mean
  *             (LAYER)
- * in FP32; r is rounded to its type first, and y is of the rounded r.  x,
- * residual, r, y [rows][cols] of `type`, row strides in elements, any
- * alignment of the element type.  gate [gate_rows][cols] of gate_type: row i
+ * in FP32 (a row whose squares leave its range is normalised to 0); r is rounded
+ * to its type first, and y is of the rounded r.  x, residual, r, y [rows][cols]
+ * of `type`, row strides in elements, any alignment of the element type.  gate [gate_rows][cols] of gate_type: row i
  * for rows [i, i + 1) rows / gate_rows; gate_rows divides rows; its row stride
  * may be 0.  Weights [cols] of their types.  1 <= cols <= 8192.
  *
