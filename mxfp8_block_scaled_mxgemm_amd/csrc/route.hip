@@ -644,7 +644,15 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
 // Gradient to the logits, with g_j = scale d_weights_j and w the weights over
 // their scale: normalised softmax w_j (g_j - <g w>); softmax s_e (g_e - <g s>)
 // over all experts; sigmoid g_j s_j (1 - s_j), normalised with (g_j - <g w>) /
-// sum s for g_j.  In 64 bits: g - <g w> cancels where one choice has all weight.
+// sum s for g_j.  In 64 bits: g - <g w> cancels where one choice has most weight.
+
+// (g - <g w>) times the sum of scores, dot = <g score>: two products, not one and a
+// multiply-add, so that nothing is left where one choice has all weight.
+__device__ __forceinline__ double from_mean(double g, double all, double dot)
+{
+#pragma clang fp contract(off)
+    return g * all - dot;
+}
 
 // The gradient of one choice: lane j of those that share a token has its logit,
 // g_j and whether it was chosen; sums over them by `sum`, maximum by `largest`.
@@ -658,12 +666,12 @@ __device__ __forceinline__ double choice_gradient(const RouteArgs& p, float logi
         if (!p.normalize)
             return g * slope;
         const double all = sum(score), dot = sum(g * score), part = all > 0.0 ? reciprocal64(all) : 0.0;
-        return (g - dot * part) * (part * slope);       // (1 / the sum may be 1e304)
+        return from_mean(g, all, dot) * part * (part * slope);      // (1 / the sum may be 1e304)
     }
     const float base = largest(logit);
     const double e = exp64(has ? (double)logit - (double)base : 0.0), score = has ? e : 0.0;
     const double all = sum(score), dot = sum(g * score), part = all > 0.0 ? reciprocal64(all) : 0.0;
-    return score * part * (g - dot * part);
+    return score * part * (from_mean(g, all, dot) * part);
 }
 
 // Where only the chosen logits have a gradient, sixteen lanes per token as above:

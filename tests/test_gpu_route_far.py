@@ -31,3 +31,18 @@ def test_normalised_sigmoids_of_far_logits(T, E, k, size):
     # 64-bit arithmetic on terms up to |d| (products of 1e-6 and a score are
     # subnormal and keep 36 bits), then float32
     mc.assert_within(got, ref, 2.0 ** -34 * d.double().abs().max() + bc.U * ref.abs(), "d_logits")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(300, 64, 1), (40, 300, 1), (40, 600, 20)])
+def test_the_only_choice_has_no_gradient(T, E, k, score):
+    """Normalised, the weight of a token's only expert is the scale whatever its
+    logit is, and the gradient zero, not what two roundings leave of it."""
+    torch_cuda()
+    g = torch.Generator().manual_seed(T)
+    x, d = 3 * torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    say(f"one choice T={T} E={E} k={k} {score}")
+    ids, _ = pkg.route_tokens(x.cuda(), k, score=score, scale=2.5)
+    ids[:, 1:] = -1
+    got = pkg.route_tokens_backward(d.cuda(), x.cuda(), ids, score=score, scale=2.5)
+    assert not got.any(), float(got.abs().max())
