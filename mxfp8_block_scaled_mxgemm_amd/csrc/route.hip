@@ -360,9 +360,9 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs p)
 // are whole lanes: a power of two of them each.  Keys are formed in FP32 first.
 // Only where a choice hangs on less than they are good for, two keys or two
 // groups' ranks nearer than `Near` says, does the wave choose by keys in 64 bits.
-// 16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 22 to 24 us, where
+// 16384 tokens of 256 experts in 8 groups, sigmoid, bias, k 8: 22 to 25 us, where
 // the 18 MB that move take 3.5.  They are one generation of four waves per SIMD,
-// which wait 61% of their time for their own chains (of 65536 tokens, 68 us, each
+// which wait 62% of their time for their own chains (of 65536 tokens, 68 us, each
 // 16384 more take 15).  With the gradient's kernel of this kind 29 us, against 48
 // with a wave to a token in both.
 struct Near {
