@@ -154,9 +154,10 @@ int mxgemm_block_linear(const mxgemm_block_linear_t* args, void* stream);
  *             (LAYER)
  * in FP32 (a row whose squares leave its range is normalised to 0); r is rounded
  * to its type first, and y is of the rounded r.  x, residual, r, y [rows][cols]
- * of `type`, row strides in elements, any alignment of the element type.  gate [gate_rows][cols] of gate_type: row i
- * for rows [i, i + 1) rows / gate_rows; gate_rows divides rows; its row stride
- * may be 0.  Weights [cols] of their types.  1 <= cols <= 8192.
+ * of `type`, row strides in elements, any alignment of the element type.  gate
+ * [gate_rows][cols] of gate_type: row i for rows [i, i + 1) rows / gate_rows;
+ * gate_rows divides rows; its row stride may be 0.  Weights [cols] of their types.
+ * 1 <= cols <= 8192.
  *
  * Gradient, from d_y and d_r (either may be NULL: zero), x, and r as it was
  * written: d_x and d_residual (or NULL) of `type`, d_gate [gate_rows][cols] of
